@@ -8,7 +8,7 @@ passed) or raw integer device addresses; ``stream`` may be a
 current stream.  The library is loaded on first use; if it has not been
 built this raises -- there is no CPU fallback.
 
-The helpers at the bottom (``frame``, ``global_``, ``sga``) allocate the
+The helpers at the bottom (``frame``, ``global_``, ``sga``, ``cached``, ...) allocate the
 outputs with torch, call the entry points and raise ``VggtError`` on a
 non-zero status.
 """
@@ -54,6 +54,23 @@ class vggt_layer(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("s_h", ctypes.c_int32), ("s_w", ctypes.c_int32)]
 
 
+class vggt_cache(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class vggt_norm(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int64), ("n_cols", ctypes.c_int32), ("kind", ctypes.c_int32),
+                ("x_fp32", ctypes.c_int32), ("post_norm", ctypes.c_int32), ("rows_per_gate", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("h_stride", ctypes.c_int64)]
+
+
+VGGT_NORM_LAYER, VGGT_NORM_RMS = 0, 1
+_NORM_KINDS = {"layer": VGGT_NORM_LAYER, "rms": VGGT_NORM_RMS}
+
 VGGT_LAYER_FRAME, VGGT_LAYER_GLOBAL, VGGT_LAYER_SGA, VGGT_LAYER_REGISTER = 0, 1, 2, 3
 _LAYER_KINDS = {"frame": VGGT_LAYER_FRAME, "global": VGGT_LAYER_GLOBAL, "sga": VGGT_LAYER_SGA,
                 "register": VGGT_LAYER_REGISTER}
@@ -80,7 +97,7 @@ def load_library(path: str):
         raise RuntimeError(f"{path} is not built; run `python -m feed_forward_view_vggt_b200.build{flag}`")
     lib = ctypes.CDLL(path)
     i32, i64, sz, vp, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
-    S = vggt_shape
+    S, CA = vggt_shape, vggt_cache
     sigs = {
         "vggt_status_string": ([i32], ctypes.c_char_p),
         "vggt_abi_version": ([], i32),
@@ -106,6 +123,11 @@ def load_library(path: str):
         "vggt_out_proj": ([vp, vp, vp, vp, S, vp], i32),
         "vggt_attn_schedule": ([vp, vp, vp, vp, S, vp, i32, f32, vp, sz, vp], i32),
         "vggt_debug_checks": ([], i32),
+        "vggt_cache_plan": ([CA, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp, vp], i32),
+        "vggt_cache_append": ([CA, vp, vp, i64, i64, vp, i32, vp, vp, vp], i32),
+        "vggt_attn_cached_workspace_bytes": ([CA, i32], sz),
+        "vggt_attn_cached": ([CA, vp, i64, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, sz, f32, vp], i32),
+        "vggt_norm_residual": ([vggt_norm, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -347,6 +369,61 @@ def vggt_out_proj(o, w, bias, y, shape, stream=None) -> int:
                                     _shape(shape), _stream(stream)))
 
 
+def _rows_ptr(x, dtype, name):
+    """As _ptr for a tensor whose rows may be strided (the last dimension is contiguous)."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_cuda:
+        raise ValueError(f"{name}: tensor must live on a CUDA device")
+    if x.stride(-1) != 1 and x.shape[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if x.dtype != dtype:
+        raise ValueError(f"{name}: expected dtype {dtype}, got {x.dtype}")
+    return x.data_ptr()
+
+
+def vggt_cache_plan(cache, cached_lens, new_lens, free_pages, free_capacity, n_free, block_table, n_rows, cu_rows,
+                    kv_lens, slots, counts, stream=None) -> int:
+    i = _i32()
+    return int(load().vggt_cache_plan(cache, _ptr(cached_lens, i, "cached_lens"), _ptr(new_lens, i, "new_lens"),
+                                      _ptr(free_pages, i, "free_pages"), int(free_capacity),
+                                      _ptr(n_free, i, "n_free"), _ptr(block_table, i, "block_table"), int(n_rows),
+                                      _ptr(cu_rows, i, "cu_rows"), _ptr(kv_lens, i, "kv_lens"),
+                                      _ptr(slots, i, "slots"), _ptr(counts, i, "counts"), _stream(stream)))
+
+
+def vggt_cache_append(cache, k, v, row_stride, in_head_stride, slots, n_rows, k_pages, v_pages, stream=None) -> int:
+    b = _bf16()
+    return int(load().vggt_cache_append(cache, _rows_ptr(k, b, "k"), _rows_ptr(v, b, "v"), int(row_stride),
+                                        int(in_head_stride), _ptr(slots, _i32(), "slots"), int(n_rows),
+                                        _rows_ptr(k_pages, b, "k_pages"), _rows_ptr(v_pages, b, "v_pages"),
+                                        _stream(stream)))
+
+
+def vggt_attn_cached_workspace_bytes(cache, n_rows) -> int:
+    return int(load().vggt_attn_cached_workspace_bytes(cache, int(n_rows)))
+
+
+def vggt_attn_cached(cache, q, q_row_stride, q_head_stride, k_pages, v_pages, block_table, cu_rows, kv_lens, n_rows,
+                     causal_unit, o, lse, workspace, workspace_bytes, scale, stream=None) -> int:
+    b, i = _bf16(), _i32()
+    return int(load().vggt_attn_cached(cache, _rows_ptr(q, b, "q"), int(q_row_stride), int(q_head_stride),
+                                       _rows_ptr(k_pages, b, "k_pages"), _rows_ptr(v_pages, b, "v_pages"),
+                                       _ptr(block_table, i, "block_table"), _ptr(cu_rows, i, "cu_rows"),
+                                       _ptr(kv_lens, i, "kv_lens"), int(n_rows), int(causal_unit), _ptr(o, b, "o"),
+                                       _ptr(lse, _f32(), "lse"), _ptr(workspace, None, "workspace"),
+                                       int(workspace_bytes), float(scale), _stream(stream)))
+
+
+def vggt_norm_residual(norm, x, y, post_w, post_b, scale, gate, w, b, x_out, h, stream=None) -> int:
+    f, t = _f32(), _f32() if norm.x_fp32 else _bf16()
+    return int(load().vggt_norm_residual(norm, _rows_ptr(x, t, "x"), _rows_ptr(y, _bf16(), "y"),
+                                         _ptr(post_w, f, "post_w"), _ptr(post_b, f, "post_b"),
+                                         _ptr(scale, f, "scale"), _ptr(gate, _bf16(), "gate"), _ptr(w, f, "w"),
+                                         _ptr(b, f, "b"), _rows_ptr(x_out, t, "x_out"),
+                                         _rows_ptr(h, _bf16(), "h"), _stream(stream)))
+
+
 def vggt_check(stream=None):
     """(status, detail word); synchronises the stream."""
     detail = ctypes.c_uint32(0)
@@ -479,3 +556,199 @@ def out_proj(o, w, shape, bias=None, stream=None):
     y = torch.empty(o.shape[0], sh.n_heads * sh.head_dim, dtype=o.dtype, device=o.device)
     _raise(vggt_out_proj(o, w, bias, y, sh, stream), "vggt_out_proj")
     return y
+
+
+# ------------------------------------------------------- streaming (paged cache)
+
+def _on(first, *others):
+    """The device of the call: all its tensors live there, and it is made current for the launch."""
+    import contextlib
+
+    import torch
+
+    for x in others:
+        if x is not None and x.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {x.device}")
+    if not first.is_cuda:
+        raise ValueError("tensors must live on a CUDA device")
+    if first.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(first.device)
+
+
+def _lent(x, stream):
+    """A buffer allocated on torch's current stream and used on `stream`: freed only after that work."""
+    if stream is not None:
+        import torch
+
+        x.record_stream(torch.cuda.ExternalStream(_stream(stream)) if isinstance(stream, int) else stream)
+    return x
+
+
+def _expect(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _page_layout(k_pages, v_pages, n_heads, n_seqs, max_pages):
+    _expect(k_pages.dim() == 4 and k_pages.shape == v_pages.shape and k_pages.stride() == v_pages.stride(),
+            "k_pages, v_pages: [n_pages, n_kv_heads, page_size, head_dim] of the same strides")
+    n_pages, n_kv_heads, page_size, head_dim = k_pages.shape
+    sp, sh, st, _ = k_pages.stride()
+    sp, sh = sp if n_pages > 1 else 64, sh if n_kv_heads > 1 else 64  # a single page or head has no stride
+    return vggt_cache(n_seqs, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, sp, sh, st)
+
+
+def cache_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size, n_rows, n_pages=None, stream=None):
+    """Plans a step: writes the pages it takes into block_table and returns
+    (cu_rows, kv_lens, slots, counts), all int32 on the device; counts is
+    [free pages left, sequences refused] and counts[:1] the next step's n_free.
+    n_rows: rows of the step's packed buffers (>= the new rows).  n_pages: pages
+    of the cache (default: as many as 32-bit slots allow)."""
+    import torch
+
+    _expect(block_table.dim() == 2 and cached_lens.numel() == new_lens.numel() == block_table.shape[0]
+            and n_free.numel() == 1, "one cached length, new length and row of block_table per sequence, one n_free")
+    seqs, max_pages = block_table.shape
+    if n_pages is None:
+        n_pages = (2 ** 31 - 1) // page_size if page_size > 0 else 1
+    cache = vggt_cache(seqs, 1, 1, 64, page_size, n_pages, max_pages, 64, 64, 64)
+    with _on(block_table, cached_lens, new_lens, free_pages, n_free):
+        # one buffer: every part starts on 4 bytes, which is all that is asked
+        out = _lent(torch.empty(2 * seqs + 3 + n_rows, dtype=torch.int32, device=block_table.device), stream)
+        counts, cu_rows, kv_lens, slots = out.split([2, seqs + 1, seqs, n_rows])
+        _raise(vggt_cache_plan(cache, cached_lens, new_lens, free_pages, free_pages.numel(), n_free, block_table,
+                               n_rows, cu_rows, kv_lens, slots, counts, stream), "vggt_cache_plan")
+    return cu_rows, kv_lens, slots, counts
+
+
+def cache_append(k, v, slots, k_pages, v_pages, stream=None):
+    """Writes the rows of k and v ([n_rows, n_kv_heads, 64], rows and heads may
+    be strided) into their slots of k_pages and v_pages."""
+    _expect(k.dim() == 3 and k.shape == v.shape and k.stride() == v.stride() and slots.shape == k.shape[:1]
+            and k.shape[1] == k_pages.shape[1] and k.shape[2] == k_pages.shape[3],
+            "k, v: [n_rows, n_kv_heads, head_dim] of the same strides, one slot per row")
+    cache = _page_layout(k_pages, v_pages, k.shape[1], 1, 1)
+    with _on(k_pages, v_pages, k, v, slots):
+        _raise(vggt_cache_append(cache, k, v, *_row_strides(k), slots, k.shape[0], k_pages, v_pages, stream),
+               "vggt_cache_append")
+
+
+def _row_strides(x):
+    # a dimension of one element has no stride of its own: any valid one does
+    row, head, _ = x.stride()
+    head = head if x.shape[1] > 1 else 64
+    return (row if x.shape[0] > 1 else max(64, head * x.shape[1])), head
+
+
+def cached(q, k_pages, v_pages, block_table, cu_rows, kv_lens, causal_unit=0, scale=None, want_lse=False,
+           workspace=None, o=None, stream=None):
+    """Attention of the new rows q ([n_rows, H, 64], rows and heads may be
+    strided) over a paged cache; see vggt_attn_cached for the mask.  Rows
+    behind cu_rows[-1] keep what ``o`` holds (uninitialised if not given)."""
+    import torch
+
+    _expect(q.dim() == 3 and q.shape[2] == k_pages.shape[3], "q: [n_rows, n_heads, head_dim]")
+    _expect(block_table.dim() == 2 and kv_lens.numel() == block_table.shape[0] == cu_rows.numel() - 1,
+            "one row of block_table and one length per sequence, one row offset more")
+    _expect(o is None or o.shape == q.shape, "o: the shape of q")
+    cache = _page_layout(k_pages, v_pages, q.shape[1], *block_table.shape)
+    with _on(q, k_pages, v_pages, block_table, cu_rows, kv_lens, workspace, o):
+        if o is None:
+            o = _lent(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
+        lse = None
+        if want_lse:
+            lse = _lent(torch.empty(q.shape[:2], dtype=torch.float32, device=q.device), stream)
+        if workspace is None:
+            nbytes = vggt_attn_cached_workspace_bytes(cache, q.shape[0])
+            if nbytes:
+                workspace = _lent(torch.empty(nbytes, dtype=torch.uint8, device=q.device), stream)
+        else:
+            nbytes = workspace.numel() * workspace.element_size()
+        _raise(vggt_attn_cached(cache, q, *_row_strides(q), k_pages, v_pages, block_table, cu_rows, kv_lens,
+                                q.shape[0], causal_unit, o, lse, workspace, nbytes,
+                                default_scale(q.shape[2]) if scale is None else scale, stream), "vggt_attn_cached")
+    return (o, lse) if want_lse else o
+
+
+def norm_residual(x, y=None, kind="layer", eps=1e-6, scale=None, gate=None, rows_per_gate=0, post_norm=False,
+                  post_weight=None, post_bias=None, weight=None, bias=None, want_h=True, inplace=False, stream=None):
+    """x' = x + scale * gate * N_post(y) and h = N_pre(x') in one pass over the
+    rows of x and y ([n_rows, n_cols]); returns (x', h).  Without y x' is x;
+    with want_h false h is None; with inplace x' overwrites x."""
+    import torch
+
+    _expect(x.dim() == 2 and (y is None or y.shape == x.shape), "x, y: [n_rows, n_cols]")
+    _expect(kind in _NORM_KINDS, "kind: 'layer' or 'rms'")
+    rows, cols = x.shape
+    for name, t in (("scale", scale), ("post_weight", post_weight), ("post_bias", post_bias), ("weight", weight),
+                    ("bias", bias)):
+        _expect(t is None or t.shape == (cols,), f"{name}: [n_cols]")
+    _expect(gate is None or (rows_per_gate >= 1 and gate.shape == (-(-rows // rows_per_gate), cols)),
+            "gate: [ceil(n_rows / rows_per_gate), n_cols]")
+    _expect(x.dtype in (torch.float32, torch.bfloat16), "x: float32 or bfloat16")
+    with _on(x, y, scale, gate, post_weight, post_bias, weight, bias):
+        out = None
+        if y is not None:
+            out = x if inplace else _lent(torch.empty((rows, cols), dtype=x.dtype, device=x.device), stream)
+        h = _lent(torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device), stream) if want_h else None
+        st = [cols if t is None or t.shape[0] <= 1 else t.stride(0) for t in (x, y, out, h)]
+        norm = vggt_norm(rows, cols, _NORM_KINDS[kind], x.dtype == torch.float32, bool(post_norm),
+                         rows_per_gate if gate is not None else 0, eps, *st)
+        _raise(vggt_norm_residual(norm, x, y, post_weight, post_bias, scale, gate, weight, bias, out, h, stream),
+               "vggt_norm_residual")
+    return (x if out is None else out), h
+
+
+class PagedCache:
+    """The paged K/V cache of a streaming trunk: pages for ``n_layers`` layers
+    that share one block table, the sequences' lengths and the free list, all
+    on the device.  A step is ``plan(new_lens, n_rows)``, then per layer
+    ``append(layer, k, v)`` and ``attend(layer, q)``, with the rows of the
+    sequences packed one after another."""
+
+    def __init__(self, n_pages, page_size, n_kv_heads, n_seqs, max_pages, n_layers=1, head_dim=64, device=None):
+        import torch
+
+        _expect(min(n_pages, page_size, n_kv_heads, n_seqs, max_pages, n_layers) >= 1, "sizes must be >= 1")
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.page_size = int(page_size)
+        self.pages = [tuple(torch.zeros(n_pages, n_kv_heads, page_size, head_dim, dtype=torch.bfloat16, device=device)
+                            for _ in range(2)) for _ in range(n_layers)]
+        self.block_table = torch.full((n_seqs, max_pages), -1, **i32)
+        self.kv_lens = torch.zeros(n_seqs, **i32)
+        # one entry more than the pages: where release() drops what it must not write
+        self.free_pages = torch.arange(n_pages + 1, **i32)
+        self.n_free = torch.full((1,), n_pages, **i32)
+        self.cu_rows = self.slots = None
+
+    def plan(self, new_lens, n_rows, stream=None):
+        """Plans a step of new_lens rows (int32 [n_seqs], on the device) in buffers of n_rows rows; returns the
+        number of refused sequences (int32 [1], on the device)."""
+        n_pages = self.pages[0][0].shape[0]
+        self.cu_rows, self.kv_lens, self.slots, counts = cache_plan(
+            self.kv_lens, new_lens, self.free_pages[:n_pages], self.n_free, self.block_table, self.page_size, n_rows,
+            n_pages=n_pages, stream=stream)
+        self.n_free = counts[:1]
+        return counts[1:]
+
+    def append(self, layer, k, v, stream=None):
+        """Writes the step's rows of a layer."""
+        cache_append(k, v, self.slots, *self.pages[layer], stream=stream)
+
+    def attend(self, layer, q, causal_unit=0, **more):
+        """Attention of the step's rows over a layer's cache (see ``cached``)."""
+        return cached(q, *self.pages[layer], self.block_table, self.cu_rows, self.kv_lens, causal_unit, **more)
+
+    def release(self, seq):
+        """Gives the pages of sequence ``seq`` back and empties it (on torch's current stream)."""
+        import torch
+
+        row, held = self.block_table[seq], (self.kv_lens[seq] + self.page_size - 1) // self.page_size
+        col = torch.arange(row.numel(), device=row.device)
+        at = torch.where(col < held, self.n_free + col, self.free_pages.numel() - 1)
+        self.free_pages = self.free_pages.index_put((at,), row)
+        self.n_free = (self.n_free + held).to(torch.int32)
+        self.kv_lens = self.kv_lens.clone()
+        self.kv_lens[seq] = 0

@@ -4,9 +4,10 @@
 // Bits of g_vggt_error:
 //   bit 0        a bounded wait ran out (kErrTimeout); bits 8..15 = the code
 //                of the first wait site that gave up;
-//   bit 1        (built with -DVGGT_DEBUG only) an index check failed
-//                (kErrBounds); bits 16..23 = the code of the first check
-//                site that failed.
+//   bit 1        an index check failed (kErrBounds): a slot or page of the
+//                caller's own in any build, a computed index in one built
+//                with -DVGGT_DEBUG; bits 16..23 = the code of the first
+//                check site that failed.
 // vggt_check() reads and clears the word.
 #pragma once
 #include <cstdint>
@@ -22,7 +23,9 @@ enum : uint32_t {
     kCheckMeanfillRead,  // mean-fill: token row read
     kCheckMeanfillSlot,  // mean-fill: gathered slot written
     kCheckIndexToken,    // index build: kept token id
-    kCheckQkvRow         // QKV projection epilogue: output row
+    kCheckQkvRow,        // QKV projection epilogue: output row
+    kCheckCacheSlot,     // cache append: a slot of the slot map (every build)
+    kCheckCachePage      // cached attention: a page of the block table (every build)
 };
 
 __device__ unsigned int g_vggt_error;

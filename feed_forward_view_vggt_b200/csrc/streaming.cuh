@@ -1,0 +1,393 @@
+// streaming.cuh -- host side of the streaming entry points (see
+// include/vggt_attn.h): plan and append of the paged cache, attention over
+// it, and the gated residual + norm.  Part of vggt_attn.cu, whose helpers it
+// uses.
+#pragma once
+
+namespace {
+
+bool aligned4(const void *p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
+bool stride_ok(int64_t s, int64_t least)
+{
+    return s >= least && s % 8 == 0 && s < (int64_t{1} << 38);
+}
+
+// Elements from the first to behind the last of a strided [rows, heads, 64].
+int64_t span(int64_t rows, int64_t row_stride, int64_t heads, int64_t head_stride)
+{
+    return (rows - 1) * row_stride + (heads - 1) * head_stride + vggt::kHeadDim;
+}
+
+vggt_status check_tables(const vggt_cache &c)
+{
+    if (c.n_seqs < 1 || c.page_size < 1 || c.n_pages < 1 || c.max_pages < 1)
+        return VGGT_ERR_INVALID_ARG;
+    if (c.n_seqs > vggt::kCacheMaxSeqs || c.page_size % 8 != 0 ||
+        static_cast<int64_t>(c.n_pages) * c.page_size > INT32_MAX ||
+        static_cast<int64_t>(c.max_pages) * c.page_size > INT32_MAX - 1024)
+        return VGGT_ERR_UNSUPPORTED;
+    return VGGT_OK;
+}
+
+vggt_status check_cache(const vggt_cache &c)
+{
+    const vggt_status st = check_tables(c);
+    if (st != VGGT_OK)
+        return st;
+    if (c.n_heads < 1 || c.n_kv_heads < 1 || c.n_heads % c.n_kv_heads != 0 || c.head_dim < 1)
+        return VGGT_ERR_INVALID_ARG;
+    if (c.head_dim != vggt::kHeadDim || c.n_heads > 64)
+        return VGGT_ERR_UNSUPPORTED;
+    if (!stride_ok(c.page_stride, vggt::kHeadDim) || !stride_ok(c.head_stride, vggt::kHeadDim) ||
+        !stride_ok(c.token_stride, vggt::kHeadDim))
+        return VGGT_ERR_INVALID_ARG;
+    return VGGT_OK;
+}
+
+size_t pool_bytes(const vggt_cache &c)
+{
+    return 2 * static_cast<size_t>((c.n_pages - 1) * c.page_stride + (c.page_size - 1) * c.token_stride +
+                                   (c.n_kv_heads - 1) * c.head_stride + vggt::kHeadDim);
+}
+
+vggt_status launched()
+{
+    return cudaGetLastError() == cudaSuccess ? VGGT_OK : VGGT_ERR_CUDA;
+}
+
+vggt_status num_sms_of(int &num_sms)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return VGGT_ERR_CUDA;
+    return VGGT_OK;
+}
+
+} // namespace
+
+VGGT_API vggt_status vggt_cache_plan(vggt_cache cache, const int32_t *cached_lens, const int32_t *new_lens,
+                                     const int32_t *free_pages, int32_t free_capacity, const int32_t *n_free,
+                                     int32_t *block_table, int32_t n_rows, int32_t *cu_rows, int32_t *kv_lens,
+                                     int32_t *slots, int32_t *counts, void *stream)
+{
+    vggt_status st = check_tables(cache);
+    if (st != VGGT_OK)
+        return st;
+    if (n_rows < 0 || free_capacity < 0)
+        return VGGT_ERR_INVALID_ARG;
+    if (n_rows > INT32_MAX - 1024)
+        return VGGT_ERR_UNSUPPORTED;
+    const size_t B = static_cast<size_t>(cache.n_seqs);
+    const void *in[4] = {cached_lens, new_lens, n_free, free_pages};
+    const size_t in_bytes[4] = {4 * B, 4 * B, 4, 4 * static_cast<size_t>(free_capacity)};
+    const void *out[5] = {block_table, cu_rows, kv_lens, counts, slots};
+    const size_t out_bytes[5] = {4 * B * cache.max_pages, 4 * (B + 1), 4 * B, 8, 4 * static_cast<size_t>(n_rows)};
+    for (int i = 0; i < 4; ++i)
+        if ((!in[i] && in_bytes[i] > 0) || !aligned4(in[i]))
+            return VGGT_ERR_INVALID_ARG;
+    for (int i = 0; i < 5; ++i) {
+        if ((!out[i] && out_bytes[i] > 0) || !aligned4(out[i]))
+            return VGGT_ERR_INVALID_ARG;
+        for (int j = 0; j < 4; ++j)
+            if (overlaps(out[i], out_bytes[i], in[j], in_bytes[j]))
+                return VGGT_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i], out_bytes[i], out[j], out_bytes[j]))
+                return VGGT_ERR_INVALID_ARG;
+    }
+    vggt::PlanParams p;
+    p.n_seqs = cache.n_seqs;
+    p.page_size = cache.page_size;
+    p.n_pages = cache.n_pages;
+    p.max_pages = cache.max_pages;
+    p.n_rows = n_rows;
+    p.free_capacity = free_capacity;
+    p.cached = cached_lens;
+    p.fresh = new_lens;
+    p.free_pages = free_pages;
+    p.n_free = n_free;
+    p.table = block_table;
+    p.cu_rows = cu_rows;
+    p.kv_lens = kv_lens;
+    p.slots = slots;
+    p.counts = counts;
+    const int64_t want = (static_cast<int64_t>(n_rows) + 4 * vggt::kPlanThreads - 1) / (4 * vggt::kPlanThreads);
+    const int grid = static_cast<int>(want < 1 ? 1 : (want > 592 ? 592 : want));
+    const size_t smem = 3 * B * sizeof(int);
+    if (smem > 40 * 1024 &&  // with the static part above 48 KB
+        cudaFuncSetAttribute(vggt::cache_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             3 * vggt::kCacheMaxSeqs * static_cast<int>(sizeof(int))) != cudaSuccess)
+        return VGGT_ERR_CUDA;
+    vggt::cache_plan_kernel<<<grid, vggt::kPlanThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched();
+}
+
+VGGT_API vggt_status vggt_cache_append(vggt_cache cache, const void *k, const void *v, int64_t row_stride,
+                                       int64_t in_head_stride, const int32_t *slots, int32_t n_rows, void *k_pages,
+                                       void *v_pages, void *stream)
+{
+    vggt_status st = check_cache(cache);
+    if (st != VGGT_OK)
+        return st;
+    if (n_rows < 0 || !stride_ok(row_stride, vggt::kHeadDim) || !stride_ok(in_head_stride, vggt::kHeadDim))
+        return VGGT_ERR_INVALID_ARG;
+    if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages) || k_pages == v_pages)
+        return VGGT_ERR_INVALID_ARG;
+    if (n_rows == 0)
+        return VGGT_OK;
+    if (!k || !v || !slots || !aligned16(k) || !aligned16(v) || !aligned4(slots))
+        return VGGT_ERR_INVALID_ARG;
+    const size_t pool = pool_bytes(cache), sb = 4 * static_cast<size_t>(n_rows);
+    const size_t rows = 2 * static_cast<size_t>(span(n_rows, row_stride, cache.n_kv_heads, in_head_stride));
+    for (const void *out : {k_pages, v_pages})
+        if (overlaps(out, pool, k, rows) || overlaps(out, pool, v, rows) || overlaps(out, pool, slots, sb))
+            return VGGT_ERR_INVALID_ARG;
+    int num_sms = 0;
+    if ((st = num_sms_of(num_sms)) != VGGT_OK)
+        return st;
+    vggt::AppendParams p;
+    p.n_rows = n_rows;
+    p.vecs = cache.n_kv_heads * 8;
+    p.page_size = cache.page_size;
+    p.n_slots = cache.n_pages * cache.page_size;
+    p.row_stride = row_stride / 8;
+    p.in_head_stride = in_head_stride / 8;
+    p.page_stride = cache.page_stride / 8;
+    p.head_stride = cache.head_stride / 8;
+    p.token_stride = cache.token_stride / 8;
+    p.k = static_cast<const uint4 *>(k);
+    p.v = static_cast<const uint4 *>(v);
+    p.k_pages = static_cast<uint4 *>(k_pages);
+    p.v_pages = static_cast<uint4 *>(v_pages);
+    p.slots = slots;
+    const int64_t blocks = (static_cast<int64_t>(n_rows) * p.vecs + 255) / 256, most = 8 * static_cast<int64_t>(num_sms);
+    vggt::cache_append_kernel<<<static_cast<int>(blocks < most ? blocks : most), 256, 0,
+                                static_cast<cudaStream_t>(stream)>>>(p);
+    return launched();
+}
+
+namespace {
+
+// Most parts a row's keys are split into.  With the fewest work items that
+// n_rows rows can make (pairs of 128-row tiles of one sequence), that many
+// parts give every SM about eight, whatever the lengths; 64 parts are enough
+// for one sequence of one key head.  Fixed by sizes alone, so that the
+// workspace size needs no device.
+int split_cap(const vggt_cache &c, int64_t n_rows)
+{
+    const int64_t tiles = (static_cast<int64_t>(c.max_pages) * c.page_size + vggt::kBlockN - 1) / vggt::kBlockN;
+    const int64_t tokens = 2 * (vggt::kBlockM / (c.n_heads / c.n_kv_heads));
+    const int64_t items = c.n_kv_heads * ((n_rows + tokens - 1) / tokens);
+    int64_t cap = (8 * 148 + items - 1) / items;
+    cap = cap < 64 ? cap : 64;
+    return static_cast<int>(cap < tiles ? cap : tiles);
+}
+
+// Workspace: 256 bytes of header, (m, l) of every part of every row and
+// head, float2 [cap][n_rows * H], and its sum of P V, float [cap][n_rows * H][64].
+struct CachedLayout {
+    size_t ml, po, total;
+};
+
+CachedLayout cached_layout(const vggt_cache &c, int64_t n_rows, int cap)
+{
+    const size_t rows = static_cast<size_t>(n_rows) * c.n_heads;
+    CachedLayout l;
+    l.ml = 256;
+    l.po = align256(l.ml + cap * rows * 8);
+    l.total = align256(l.po + cap * rows * vggt::kHeadDim * 4);
+    return l;
+}
+
+} // namespace
+
+VGGT_API size_t vggt_attn_cached_workspace_bytes(vggt_cache cache, int32_t n_rows)
+{
+    if (check_cache(cache) != VGGT_OK || n_rows < 1)
+        return 0;
+    const int cap = split_cap(cache, n_rows);
+    return cap > 1 ? cached_layout(cache, n_rows, cap).total : 0;
+}
+
+VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                                      const void *k_pages, const void *v_pages, const int32_t *block_table,
+                                      const int32_t *cu_rows, const int32_t *kv_lens, int32_t n_rows,
+                                      int32_t causal_unit, void *o, float *lse, void *workspace,
+                                      size_t workspace_bytes, float scale, void *stream)
+{
+    vggt_status st = check_cache(cache);
+    if (st != VGGT_OK)
+        return st;
+    if (n_rows < 0 || causal_unit < 0 || !scale_ok(scale) || !stride_ok(q_row_stride, vggt::kHeadDim) ||
+        !stride_ok(q_head_stride, vggt::kHeadDim))
+        return VGGT_ERR_INVALID_ARG;
+    if (n_rows > INT32_MAX - 1024)
+        return VGGT_ERR_UNSUPPORTED;
+    if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages) || !block_table || !cu_rows || !kv_lens ||
+        !aligned4(block_table) || !aligned4(cu_rows) || !aligned4(kv_lens))
+        return VGGT_ERR_INVALID_ARG;
+    if (n_rows == 0)
+        return VGGT_OK;
+    if (!q || !o || !aligned16(q) || !aligned16(o) || !aligned4(lse))
+        return VGGT_ERR_INVALID_ARG;
+    const size_t need = vggt_attn_cached_workspace_bytes(cache, n_rows);
+    if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return VGGT_ERR_INVALID_ARG;
+    if (workspace_bytes < need)
+        return VGGT_ERR_WORKSPACE;
+    const size_t rows = static_cast<size_t>(n_rows) * cache.n_heads, B = static_cast<size_t>(cache.n_seqs);
+    const void *in[6] = {q, k_pages, v_pages, block_table, cu_rows, kv_lens};
+    const size_t in_bytes[6] = {2 * static_cast<size_t>(span(n_rows, q_row_stride, cache.n_heads, q_head_stride)),
+                                pool_bytes(cache), pool_bytes(cache), 4 * B * cache.max_pages, 4 * (B + 1), 4 * B};
+    const void *out[3] = {o, lse, workspace};
+    const size_t out_bytes[3] = {rows * vggt::kHeadDim * 2, lse ? rows * 4 : 0, need};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < 6; ++j)
+            if (out_bytes[i] > 0 && overlaps(out[i], out_bytes[i], in[j], in_bytes[j]))
+                return VGGT_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (out_bytes[i] > 0 && out_bytes[j] > 0 && overlaps(out[i], out_bytes[i], out[j], out_bytes[j]))
+                return VGGT_ERR_INVALID_ARG;
+    }
+    vggt::CachedParams p;
+    std::memset(&p, 0, sizeof p);
+    p.n_seqs = cache.n_seqs;
+    p.n_rows = n_rows;
+    p.H = cache.n_heads;
+    p.Hkv = cache.n_kv_heads;
+    p.page_size = cache.page_size;
+    p.n_pages = cache.n_pages;
+    p.max_pages = cache.max_pages;
+    p.unit = causal_unit;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.q_row_stride = q_row_stride;
+    p.q_head_stride = q_head_stride;
+    p.page_stride = cache.page_stride;
+    p.head_stride = cache.head_stride;
+    p.token_stride = cache.token_stride;
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k_pages = static_cast<const __nv_bfloat16 *>(k_pages);
+    p.v_pages = static_cast<const __nv_bfloat16 *>(v_pages);
+    p.table = block_table;
+    p.cu_rows = cu_rows;
+    p.kv_lens = kv_lens;
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.lse = lse;
+    const int64_t blocks = (static_cast<int64_t>(n_rows) * cache.n_heads + 3) / 4;
+    if (blocks > INT32_MAX)
+        return VGGT_ERR_UNSUPPORTED;
+    vggt::cached_attn_kernel<<<static_cast<unsigned>(blocks), 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched();
+}
+
+namespace {
+
+template <typename X, int kVec, int kWarps>
+void launch_norm(const vggt::NormParams &p, cudaStream_t s)
+{
+    constexpr int rows = kWarps > 4 ? 1 : 4 / kWarps;
+    vggt::norm_residual_kernel<X, kVec, kWarps>
+        <<<static_cast<unsigned>((p.n_rows + rows - 1) / rows), 32 * kWarps * rows, 0, s>>>(p);
+}
+
+template <typename X>
+void launch_norm_cols(const vggt::NormParams &p, cudaStream_t s)
+{
+    if (p.n_cols <= 256)
+        launch_norm<X, 1, 1>(p, s);
+    else if (p.n_cols <= 512)
+        launch_norm<X, 2, 1>(p, s);
+    else if (p.n_cols <= 1024)
+        launch_norm<X, 4, 1>(p, s);
+    else if (p.n_cols <= 4096)
+        launch_norm<X, 4, 4>(p, s);
+    else
+        launch_norm<X, 4, 8>(p, s);
+}
+
+} // namespace
+
+VGGT_API vggt_status vggt_norm_residual(vggt_norm norm, const void *x, const void *y, const float *post_w,
+                                        const float *post_b, const float *scale, const void *gate, const float *w,
+                                        const float *b, void *x_out, void *h, void *stream)
+{
+    if (norm.n_rows < 0 || norm.n_cols < 1 || (norm.kind != VGGT_NORM_LAYER && norm.kind != VGGT_NORM_RMS) ||
+        (norm.x_fp32 != 0 && norm.x_fp32 != 1) || (norm.post_norm != 0 && norm.post_norm != 1) ||
+        !std::isfinite(norm.eps) || norm.eps < 0.f)
+        return VGGT_ERR_INVALID_ARG;
+    if (norm.n_cols % 8 != 0 || norm.n_cols > vggt::kNormMaxCols || norm.n_rows > INT32_MAX - 1024)
+        return VGGT_ERR_UNSUPPORTED;
+    if (!y && (post_w || post_b || scale || gate || x_out || norm.post_norm))
+        return VGGT_ERR_INVALID_ARG;
+    if ((!norm.post_norm && (post_w || post_b)) || (!h && (w || b)) || (!x_out && !h))
+        return VGGT_ERR_INVALID_ARG;
+    if (gate && norm.rows_per_gate < 1)
+        return VGGT_ERR_INVALID_ARG;
+    const int64_t C = norm.n_cols, R = norm.n_rows;
+    if (!stride_ok(norm.x_stride, C) || (y && !stride_ok(norm.y_stride, C)) ||
+        (x_out && !stride_ok(norm.out_stride, C)) || (h && !stride_ok(norm.h_stride, C)))
+        return VGGT_ERR_INVALID_ARG;
+    if (R == 0)
+        return VGGT_OK;
+    if (!x)
+        return VGGT_ERR_INVALID_ARG;
+    const size_t xw = norm.x_fp32 ? 4 : 2;
+    auto bytes = [&](const void *ptr, int64_t stride, size_t width) {
+        return ptr ? static_cast<size_t>((R - 1) * stride + C) * width : size_t{0};
+    };
+    const size_t cb = static_cast<size_t>(C) * 4;
+    const int64_t gates = gate ? (R + norm.rows_per_gate - 1) / norm.rows_per_gate : 0;
+    const void *in[8] = {x, y, post_w, post_b, scale, gate, w, b};
+    const size_t in_bytes[8] = {bytes(x, norm.x_stride, xw), bytes(y, norm.y_stride, 2), cb, cb, cb,
+                                static_cast<size_t>(gates * C) * 2, cb, cb};
+    const void *out[2] = {x_out, h};
+    const size_t out_bytes[2] = {bytes(x_out, norm.out_stride, xw), bytes(h, norm.h_stride, 2)};
+    for (int i = 0; i < 8; ++i)
+        if (!aligned16(in[i]))
+            return VGGT_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i) {
+        if (!aligned16(out[i]))
+            return VGGT_ERR_INVALID_ARG;
+        for (int j = 0; j < 8; ++j) {
+            if (!out[i] || !in[j] || (i == 0 && j == 0 && x_out == x && norm.out_stride == norm.x_stride))
+                continue;
+            if (overlaps(out[i], out_bytes[i], in[j], in_bytes[j]))
+                return VGGT_ERR_INVALID_ARG;
+        }
+    }
+    if (x_out && h && overlaps(x_out, out_bytes[0], h, out_bytes[1]))
+        return VGGT_ERR_INVALID_ARG;
+    vggt::NormParams p;
+    p.n_rows = R;
+    p.n_cols = norm.n_cols;
+    p.rows_per_gate = gate ? norm.rows_per_gate : 1;
+    p.layer = norm.kind == VGGT_NORM_LAYER;
+    p.post_norm = norm.post_norm;
+    p.eps = norm.eps;
+    p.inv_cols = 1.f / static_cast<float>(C);
+    p.x_stride = norm.x_stride;
+    p.y_stride = norm.y_stride;
+    p.out_stride = norm.out_stride;
+    p.h_stride = norm.h_stride;
+    p.gate_stride = C;
+    p.x = x;
+    p.y = static_cast<const __nv_bfloat16 *>(y);
+    p.gate = static_cast<const __nv_bfloat16 *>(gate);
+    p.post_w = post_w;
+    p.post_b = post_b;
+    p.scale = scale;
+    p.w = w;
+    p.b = b;
+    p.x_out = x_out;
+    p.h = static_cast<__nv_bfloat16 *>(h);
+    if (norm.x_fp32)
+        launch_norm_cols<float>(p, static_cast<cudaStream_t>(stream));
+    else
+        launch_norm_cols<__nv_bfloat16>(p, static_cast<cudaStream_t>(stream));
+    return launched();
+}

@@ -14,6 +14,9 @@
 #include "vggt_attn.h"
 
 #include "attn_kernel.cuh"
+#include "cache_kernels.cuh"
+#include "cached_attn_kernel.cuh"
+#include "norm_kernel.cuh"
 #include "qkv_kernel.cuh"
 #include "sga_kernels.cuh"
 
@@ -1259,3 +1262,5 @@ VGGT_API vggt_status vggt_attn_sga_noalloc(const void *q, const void *k, const v
     return vggt_attn_sga(q, k, v, o, lse, shape, s_h, s_w, kept_idx, mult, scratch,
                          VGGT_SGA_STATIC_SCRATCH_BYTES, scale, stream);
 }
+
+#include "streaming.cuh"

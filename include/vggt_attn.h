@@ -70,7 +70,8 @@ typedef enum {
     VGGT_ERR_WORKSPACE = 3,   /* SGA workspace smaller than vggt_sga_workspace_bytes() */
     VGGT_ERR_CUDA = 4,        /* a CUDA runtime call or launch failed */
     VGGT_ERR_TIMEOUT = 5,     /* a bounded in-kernel wait ran out (see vggt_check) */
-    VGGT_ERR_BOUNDS = 6       /* debug builds only: a device index check failed (see vggt_check) */
+    VGGT_ERR_BOUNDS = 6       /* a device index check failed: a slot or page of the caller's in any build, the
+                                 library's own indices in debug builds (see vggt_check) */
 } vggt_status;
 
 typedef struct {
@@ -335,6 +336,142 @@ vggt_status vggt_attn_schedule(const void *const *q, const void *const *k, const
                                void *const *o, vggt_shape shape, const vggt_layer *layers, int32_t n_layers,
                                float scale, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---------------------------------------------------------------------
+ * Streaming: scenes whose frames arrive over time.  Global attention reads
+ * the tokens of all views [VGGT "Alternating-Attention"]; when the views of
+ * a scene come one after another, the keys and values of the earlier ones
+ * are kept in a paged cache and only the new frames' rows are computed.
+ * The pages describe no cache; these entry points are the step of such a
+ * trunk, for several scenes (or token sequences) at once:
+ *
+ *   vggt_cache_plan      once per step: pages for the new tokens, the slot of
+ *                        every new row, row offsets, new lengths
+ *   vggt_norm_residual   per block: residual update and the next norm
+ *   vggt_qkv_rope        per layer, on the packed new rows
+ *   vggt_cache_append    per layer: the new K and V rows into their slots
+ *   vggt_attn_cached     per layer: the new rows against the cache
+ *   vggt_out_proj        per layer
+ *
+ * Rows are packed: sequence b owns rows cu_rows[b] .. cu_rows[b+1] - 1 of
+ * q, k, v and o.  A page holds page_size consecutive positions of one
+ * sequence; position t of sequence b lies in page block_table[b][t /
+ * page_size], at t % page_size; its slot is page * page_size + t %
+ * page_size.  The pages of K and of V are bf16 tensors [n_pages,
+ * n_kv_heads, page_size, 64] with any strides that are multiples of 8
+ * elements (a page-, head- or token-major cache, or K and V side by side in
+ * one buffer), the same for both. */
+typedef struct {
+    int32_t n_seqs;     /* sequences of the batch, 1..4096 */
+    int32_t n_heads;    /* query heads H, 1..64 */
+    int32_t n_kv_heads; /* key/value heads, a divisor of n_heads: query head h reads h / (H / n_kv_heads) */
+    int32_t head_dim;   /* must be 64 */
+    int32_t page_size;  /* positions per page, a multiple of 8 */
+    int32_t n_pages;    /* pages of the cache; n_pages * page_size < 2^31 */
+    int32_t max_pages;  /* columns of the block table: pages one sequence can hold; * page_size < 2^31 - 1024 */
+    int64_t page_stride, head_stride, token_stride; /* elements; multiples of 8, at least 64 */
+} vggt_cache;
+
+/* Plan of a step, from the sequences' lengths, all on the device.
+ * cached_lens, new_lens: int32 [n_seqs], positions in the cache and rows
+ * that this step adds (negative counts as 0; both may be 0).  free_pages:
+ * int32 [free_capacity], of which the first *n_free are free; n_free: int32
+ * (a value outside [0, free_capacity] is cut).  block_table: int32 [n_seqs,
+ * max_pages], in and out: its first ceil(cached / page_size) entries of a
+ * row are read, the entries of pages taken in this step are written, the
+ * others are left.  Written:
+ *   cu_rows  int32 [n_seqs + 1]  row offsets, cut at n_rows
+ *   kv_lens  int32 [n_seqs]      cached + new (a refused sequence: cached)
+ *   slots    int32 [n_rows]      slot of every row; -1 for the rows of a
+ *                                refused sequence and behind the last one
+ *   counts   int32 [2]           free pages left, sequences refused
+ * Pages are taken in sequence order from the end of the free list:
+ * free_pages[n_free - 1] first.  A sequence is refused when its rows end
+ * behind n_rows, when it would need more than max_pages pages, or when it
+ * needs a page and its needs and those of the sequences before it exceed
+ * n_free; it takes none.  The caller returns pages by writing them behind
+ * the last free one.  counts[0] may be the next step's *n_free; counts must
+ * not overlap n_free (the same step can then be planned again).  The heads
+ * and strides of `cache` are not used.  One kernel launch. */
+vggt_status vggt_cache_plan(vggt_cache cache, const int32_t *cached_lens, const int32_t *new_lens,
+                            const int32_t *free_pages, int32_t free_capacity, const int32_t *n_free,
+                            int32_t *block_table, int32_t n_rows, int32_t *cu_rows, int32_t *kv_lens,
+                            int32_t *slots, int32_t *counts, void *stream);
+
+/* New K and V rows into their slots.  k, v: bf16, row r, head h at
+ * r * row_stride + h * in_head_stride (elements, multiples of 8, at least
+ * 64: slices of one projection's rows, e.g.).  slots: int32 [n_rows], a
+ * negative one skips its row; a slot past the cache is skipped and reported
+ * by vggt_check (VGGT_ERR_BOUNDS).  Slots must be distinct (a repeated one
+ * leaves any mixture of its rows).  One kernel launch, none for n_rows = 0. */
+vggt_status vggt_cache_append(vggt_cache cache, const void *k, const void *v, int64_t row_stride,
+                              int64_t in_head_stride, const int32_t *slots, int32_t n_rows, void *k_pages,
+                              void *v_pages, void *stream);
+
+/* Attention of the new rows over the paged cache [VGGT
+ * "Alternating-Attention", global attention, with the keys of the views seen
+ * so far].  Row r of sequence b is the query of position
+ * p = kv_lens[b] - (cu_rows[b+1] - r); it sees the keys j < lim of its
+ * sequence,
+ *   causal_unit = 0: lim = kv_lens[b] (every key, e.g. a chunk against an
+ *                    encoder's states);
+ *   causal_unit = u: lim = min(kv_lens[b], (floor(p / u) + 1) * u): causal
+ *                    by units of u positions (u = L: by frame, the tokens of
+ *                    a frame see one another; u = 1: by token); 0 for p < 0.
+ * A row that sees no key gets o = 0 and lse = -inf.  Rows behind
+ * cu_rows[n_seqs] are not written.  Cache contents behind kv_lens[b] are
+ * never used, whatever they hold; keys and values before it must be finite
+ * (a non-finite value can reach rows that do not see its key).
+ * q: bf16, row r, head h at r * q_row_stride + h * q_head_stride (elements,
+ * multiples of 8, at least 64).  o: bf16 [n_rows, H, 64].  lse: optional
+ * float [n_rows, H].  block_table: int32 [n_seqs, max_pages], its first
+ * ceil(kv_lens / page_size) entries of a row are read; a page outside
+ * [0, n_pages) is not read and reported by vggt_check (VGGT_ERR_BOUNDS), the
+ * rows of its sequence are then unspecified.  cu_rows: int32 [n_seqs + 1],
+ * ascending from 0, at most n_rows.  kv_lens: int32 [n_seqs], cut at 0 and
+ * max_pages * page_size.  workspace: device, 256-byte aligned,
+ * vggt_attn_cached_workspace_bytes() bytes (0: may be NULL), overwritten;
+ * calls that may run at the same time need one each.  The lengths are read
+ * on the device: a captured call replays with the lengths of its replay.
+ * The order of the sums depends on the lengths of the whole batch, never on
+ * timing.  At most two kernel launches; none for n_rows = 0. */
+size_t vggt_attn_cached_workspace_bytes(vggt_cache cache, int32_t n_rows);
+vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q_row_stride, int64_t q_head_stride,
+                             const void *k_pages, const void *v_pages, const int32_t *block_table,
+                             const int32_t *cu_rows, const int32_t *kv_lens, int32_t n_rows, int32_t causal_unit,
+                             void *o, float *lse, void *workspace, size_t workspace_bytes, float scale,
+                             void *stream);
+
+/* The seam between two blocks in one pass over the rows:
+ *   x' = x + scale * gate * N_post(y)      (elementwise; scale the layer
+ *   h  = N_pre(x')                          scale, gate one row per group)
+ * y is a block's output (vggt_out_proj, e.g.), h the input of the next block's
+ * projection (vggt_qkv_rope).  N is a LayerNorm, (t - mean) / sqrt(var +
+ * eps) * w + b with the biased variance, or an RMSNorm, t / sqrt(mean(t^2) +
+ * eps) * w + b.  All sums are fp32; h is taken from x' before it is rounded. */
+typedef enum { VGGT_NORM_LAYER = 0, VGGT_NORM_RMS = 1 } vggt_norm_kind;
+typedef struct {
+    int64_t n_rows;        /* >= 0 */
+    int32_t n_cols;        /* channels, a multiple of 8, 8..8192 */
+    int32_t kind;          /* vggt_norm_kind, of both norms */
+    int32_t x_fp32;        /* the residual stream x, x': 0 = bf16, 1 = float */
+    int32_t post_norm;     /* 0: N_post is the identity */
+    int32_t rows_per_gate; /* gate row of row r: r / rows_per_gate; >= 1 with a gate */
+    float eps;             /* >= 0, of both norms */
+    int64_t x_stride, y_stride, out_stride, h_stride; /* row strides in elements, multiples of 8, >= n_cols */
+} vggt_norm;
+
+/* x: [n_rows, n_cols], bf16 or float.  y: bf16 or NULL (then x' = x, and
+ * post_*, scale, gate and x_out must be NULL).  post_w, post_b, scale, w, b:
+ * float [n_cols] or NULL (1 for the weights and the scale, 0 for the
+ * biases).  gate: bf16 [ceil(n_rows / rows_per_gate), n_cols] contiguous, or
+ * NULL.  x_out: x', of x's type, or NULL (not written); it may be x itself
+ * (same pointer and stride).  h: bf16, or NULL (then w and b must be NULL);
+ * one of x_out and h is needed.  Every pointer is 16-byte aligned.  No other
+ * overlap of outputs with inputs.  One kernel launch, none for n_rows = 0. */
+vggt_status vggt_norm_residual(vggt_norm norm, const void *x, const void *y, const float *post_w,
+                               const float *post_b, const float *scale, const void *gate, const float *w,
+                               const float *b, void *x_out, void *h, void *stream);
+
 /* Test hook for the failure path (the pages have no counterpart): runs
  * vggt_attn_global with the first scores of query rows 0..127 of every CTA
  * never signalled, and with every in-kernel wait bounded by wait_limit_ns
@@ -348,7 +485,8 @@ vggt_status vggt_test_attn_global_stall(const void *q, const void *k, const void
 
 /* Synchronises `stream`, then reads and clears this device's error word.
  * Returns VGGT_ERR_TIMEOUT if a bounded wait ran out in any kernel since the
- * last check, VGGT_ERR_BOUNDS if (debug build) a device index check failed,
+ * last check, VGGT_ERR_BOUNDS if a device index check failed (a slot or a
+ * page outside the cache in any build, a computed index in a debug build),
  * VGGT_ERR_CUDA if the stream reports an error, else VGGT_OK.  detail, if
  * not NULL, receives the raw word: bit 0 = timeout, bits 8..15 = the code of
  * the first wait site that gave up, bit 1 = index check, bits 16..23 = the
