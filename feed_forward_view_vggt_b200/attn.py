@@ -576,12 +576,17 @@ def _on(first, *others):
     return torch.cuda.device(first.device)
 
 
-def _lent(x, stream):
-    """A buffer allocated on torch's current stream and used on `stream`: freed only after that work."""
-    if stream is not None:
-        import torch
+def _new(shape, dtype, device, stream, returned=True):
+    """A buffer of a call on `stream`: allocated there, since memory that was freed on torch's current stream may still
+    be in use on it, and (if it is returned) freed only after the work of the current stream that reads it."""
+    import torch
 
-        x.record_stream(torch.cuda.ExternalStream(_stream(stream)) if isinstance(stream, int) else stream)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
+        x = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        x.record_stream(torch.cuda.current_stream(device))
     return x
 
 
@@ -615,7 +620,7 @@ def cache_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size
     cache = vggt_cache(seqs, 1, 1, 64, page_size, n_pages, max_pages, 64, 64, 64)
     with _on(block_table, cached_lens, new_lens, free_pages, n_free):
         # one buffer: every part starts on 4 bytes, which is all that is asked
-        out = _lent(torch.empty(2 * seqs + 3 + n_rows, dtype=torch.int32, device=block_table.device), stream)
+        out = _new(2 * seqs + 3 + n_rows, torch.int32, block_table.device, stream)
         counts, cu_rows, kv_lens, slots = out.split([2, seqs + 1, seqs, n_rows])
         _raise(vggt_cache_plan(cache, cached_lens, new_lens, free_pages, free_pages.numel(), n_free, block_table,
                                n_rows, cu_rows, kv_lens, slots, counts, stream), "vggt_cache_plan")
@@ -655,14 +660,14 @@ def cached(q, k_pages, v_pages, block_table, cu_rows, kv_lens, causal_unit=0, sc
     cache = _page_layout(k_pages, v_pages, q.shape[1], *block_table.shape)
     with _on(q, k_pages, v_pages, block_table, cu_rows, kv_lens, workspace, o):
         if o is None:
-            o = _lent(torch.empty(q.shape, dtype=q.dtype, device=q.device), stream)
+            o = _new(q.shape, q.dtype, q.device, stream)
         lse = None
         if want_lse:
-            lse = _lent(torch.empty(q.shape[:2], dtype=torch.float32, device=q.device), stream)
+            lse = _new(q.shape[:2], torch.float32, q.device, stream)
         if workspace is None:
             nbytes = vggt_attn_cached_workspace_bytes(cache, q.shape[0])
             if nbytes:
-                workspace = _lent(torch.empty(nbytes, dtype=torch.uint8, device=q.device), stream)
+                workspace = _new(nbytes, torch.uint8, q.device, stream, returned=False)
         else:
             nbytes = workspace.numel() * workspace.element_size()
         _raise(vggt_attn_cached(cache, q, *_row_strides(q), k_pages, v_pages, block_table, cu_rows, kv_lens,
@@ -690,8 +695,8 @@ def norm_residual(x, y=None, kind="layer", eps=1e-6, scale=None, gate=None, rows
     with _on(x, y, scale, gate, post_weight, post_bias, weight, bias):
         out = None
         if y is not None:
-            out = x if inplace else _lent(torch.empty((rows, cols), dtype=x.dtype, device=x.device), stream)
-        h = _lent(torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device), stream) if want_h else None
+            out = x if inplace else _new((rows, cols), x.dtype, x.device, stream)
+        h = _new((rows, cols), torch.bfloat16, x.device, stream) if want_h else None
         st = [cols if t is None or t.shape[0] <= 1 else t.stride(0) for t in (x, y, out, h)]
         norm = vggt_norm(rows, cols, _NORM_KINDS[kind], x.dtype == torch.float32, bool(post_norm),
                          rows_per_gate if gate is not None else 0, eps, *st)

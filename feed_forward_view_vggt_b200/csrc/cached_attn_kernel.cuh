@@ -1,7 +1,43 @@
 // cached_attn_kernel.cuh -- attention of a step's new rows over a paged K/V
-// cache: O_i = sum_j e^{s q_i.k_j} v_j / sum_j e^{s q_i.k_j} over the keys
-// j < lim_i of i's own sequence, lim_i = min(kv, (floor(pos_i / u) + 1) u).
+// cache on the sm_100a tensor cores:
+//   O_i = sum_j e^{s q_i.k_j} v_j / sum_j e^{s q_i.k_j},  j < lim_i,
+//   lim_i = min(kv, (floor(pos_i / u) + 1) u)   (u = 0: kv),
+// over the keys of i's own sequence, in one pass with a running offset and
+// sum of the softmax.
+//
+// Rows.  The G = H / Hkv query heads of a key head are rows of one tile: a
+// tile holds F = floor(128 / G) consecutive tokens of a sequence, G rows each,
+// so a key tile is read once for all of them.
+//
+// Work.  A task is a range of 128-key tiles of one key head for
+//  * a pair of query tiles: both read one K/V stream, one softmax warpgroup
+//    each (two steps per key tile); or
+//  * a single query tile (the last of an odd number, every single-token
+//    sequence): the warpgroups take the key tiles in turn (one step per key
+//    tile) and warpgroup 0 merges the two softmax states at the end.
+// A step costs the same in both: 4.2 MFLOP on the tensor cores, or 32 KB of
+// K and V per step of a single tile, about 0.7 us of an SM's share of either.
+// Ranges are cut to at most `steps` steps, so one sequence and few rows fill
+// the GPU too.  Every CTA finds the same `steps` from the lengths (see
+// plan_tasks): no host copy of the lengths, no launch before this one.  Tasks
+// are numbered with the pairs of a head and key range innermost and dealt out
+// in turn, so that the CTAs that read the same keys do so at the same time.
+// The parts of a cut range leave (m, l) and the sum of P V in fp32 in the
+// workspace, and cached_combine_kernel joins them in order.
+//
+// CTA (384 threads, one per SM): warp 0 loads Q, K and V by TMA, page by page
+// (a 4-D map of the pages; a box is the largest power of two of rows that
+// divides the page, at most 128), warp 1 issues the UMMAs, warp 2 decodes
+// tasks ahead into a ring, warps 4-7 and 8-11 are the softmax warpgroups.
+// TMEM, score buffers and the order S(k+3) after PV(k) are those of
+// attn_fwd_kernel.
+//
+// Keys behind kv are never used, whatever the page holds there: their scores
+// are masked, their V rows are zeroed in shared memory up to the next multiple
+// of 16 (a 0 in P does not survive an infinity in V), and the PV product of
+// the last tile stops there.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -9,111 +45,1021 @@
 #include "attn_kernel.cuh"
 #include "cache_kernels.cuh"
 #include "device_error.cuh"
+#include "ptx.cuh"
 
 namespace vggt {
 
+constexpr int kMaxSplits = 128;
+constexpr int kTaskRing = 8;
+constexpr int kNoSplit = 0x7fffffff;
+// Cost of a task beside its steps (Q load, first score, epilogue) and of the
+// joining launch, in steps: used to choose `steps` only.
+constexpr float kTaskOverhead = 4.f, kJoinOverhead = 4.f;
+
+enum : uint32_t { kSiteTaskFull = 12, kSiteTaskEmpty, kSiteMergeReady, kSiteMergeFree };
+
 struct CachedParams {
-    int n_seqs, n_rows, H, Hkv, page_size, n_pages, max_pages, unit;
+    int n_seqs, n_rows, H, Hkv, group, tile_tokens;  // group G = H / Hkv, tile_tokens F
+    int page_size, n_pages, max_pages, unit, box_rows;
+    int max_splits;  // most parts of a row's keys; 1: no workspace
     float scale_log2;
-    int64_t q_row_stride, q_head_stride;
-    int64_t page_stride, head_stride, token_stride;
-    const __nv_bfloat16 *q, *k_pages, *v_pages;
     const int32_t *table, *cu_rows, *kv_lens;
     __nv_bfloat16 *o;
     float *lse;
+    int32_t *header;  // workspace: [0] = steps
+    float2 *part_ml;  // [max_splits][n_rows * H]
+    float *part_o;    // [max_splits][n_rows * H][64]
+    unsigned long long wait_limit_ns;
 };
 
-// One warp per (row, head): 32 keys at a time, a key's logit per lane, two
-// output channels per lane, one pass with the running maximum and sum.
-__global__ void __launch_bounds__(128) cached_attn_kernel(const CachedParams p)
+struct Task {
+    int row0, row_end;  // first token row of the task's first tile, end of its sequence's rows
+    int pos0, kv;       // position of row0's token, keys of the sequence
+    int kt0, n;         // first key tile, key tiles (0: the end of the CTA's tasks)
+    int b, hk;
+    int pair, split, chunk;
+    int vlast;          // keys of the last tile that exist, 1..128
+};
+
+struct __align__(1024) CachedSmem {
+    uint8_t q[2][2][kTileBytes];  // [buffer][tile]
+    uint8_t k[kStages][kTileBytes];
+    uint8_t v[kStages][kTileBytes];
+    Task task[kTaskRing];
+    float2 merge_ml[kBlockM];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t k_full[kStages], k_empty[kStages];
+    uint64_t v_full[kStages], v_empty[kStages];
+    uint64_t s_full[2][3], p_ready[2][3];  // by warpgroup and its step count mod 3
+    uint64_t o_done[2], o_final[2];
+    uint64_t merge_ready, merge_free;
+    uint64_t task_full[kTaskRing], task_empty[kTaskRing];
+    uint64_t drain;
+    uint32_t tmem_base;
+    WaitCtl ctl;
+    int cand_tasks[kMaxSplits];
+    int longest, work, steps, n_tasks;
+    int scan[kAttnThreads / 32];
+    int task_end[1];  // [n_seqs]: tasks up to and with the sequence
+};
+
+constexpr size_t cached_smem_bytes(int n_seqs)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (id >= static_cast<int64_t>(p.n_rows) * p.H)
-        return;
-    const int row = static_cast<int>(id / p.H), h = static_cast<int>(id % p.H), hk = h / (p.H / p.Hkv);
-    int lo = 0, hi = p.n_seqs;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu_rows[mid + 1] > row)
-            hi = mid;
-        else
-            lo = mid + 1;
-    }
-    const int b = lo;
-    if (b >= p.n_seqs)
-        return;
-    const int kv = max(0, min(p.kv_lens[b], p.max_pages * p.page_size));
-    const int pos = kv - p.cu_rows[b + 1] + row;
-    int lim = kv;
-    if (p.unit > 0)
-        lim = pos < 0 ? 0
-                      : static_cast<int>(min(static_cast<int64_t>(kv),
-                                             (static_cast<int64_t>(pos / p.unit) + 1) * p.unit));
-    const __nv_bfloat16 *q = p.q + row * p.q_row_stride + h * p.q_head_stride;
-    float qv[64];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint4 x = reinterpret_cast<const uint4 *>(q)[i];
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            qv[8 * i + 2 * e] = bf16lo_to_f32(xs[e]) * p.scale_log2;
-            qv[8 * i + 2 * e + 1] = bf16hi_to_f32(xs[e]) * p.scale_log2;
+    return sizeof(CachedSmem) + 4 * static_cast<size_t>(n_seqs) + 1024;
+}
+
+// ------------------------------------------------------------ geometry
+
+struct Seq {
+    int row0, n, kv;
+};
+
+__device__ __forceinline__ Seq load_seq(const CachedParams &p, int b)
+{
+    Seq s;
+    s.row0 = max(0, min(__ldg(p.cu_rows + b), p.n_rows));
+    s.n = max(s.row0, min(__ldg(p.cu_rows + b + 1), p.n_rows)) - s.row0;
+    s.kv = max(0, min(__ldg(p.kv_lens + b), p.max_pages * p.page_size));
+    return s;
+}
+
+// Keys that the row of position pos sees.  pos + unit fits in 32 unsigned bits.
+__device__ __forceinline__ int key_limit(int kv, int pos, int unit)
+{
+    if (unit == 0)
+        return kv;
+    if (pos < 0)
+        return 0;
+    const unsigned u = static_cast<unsigned>(unit), lim = (static_cast<unsigned>(pos) / u + 1u) * u;
+    return static_cast<int>(min(static_cast<unsigned>(kv), lim));
+}
+
+// Key tiles that rows 0 .. i of a sequence see (the limit never falls with the row).
+__device__ __forceinline__ int key_tiles(const CachedParams &p, const Seq &s, int i)
+{
+    return (key_limit(s.kv, s.kv - s.n + i, p.unit) + kBlockN - 1) / kBlockN;
+}
+
+// Key tiles of query-tile pair pr.
+__device__ __forceinline__ int pair_tiles(const CachedParams &p, const Seq &s, int pr)
+{
+    return key_tiles(p, s, min(s.n, (2 * pr + 2) * p.tile_tokens) - 1);
+}
+
+__device__ __forceinline__ int parts_of(int tiles, int most)
+{
+    return tiles <= most ? 1 : (tiles - 1) / most + 1;
+}
+
+__device__ __forceinline__ int pair_step_tiles(int steps)
+{
+    return (steps >> 1) + (steps & 1);
+}
+
+// Tasks of one key head of a sequence: pairs first, then the single tile.
+struct SeqTasks {
+    int pairs, single;
+};
+
+__device__ __forceinline__ SeqTasks seq_tasks(const CachedParams &p, const Seq &s, int steps)
+{
+    SeqTasks t{0, 0};
+    if (s.n == 0)
+        return t;
+    const int tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens, pairs = tiles >> 1, c = pair_step_tiles(steps);
+    if (pairs > 0) {
+        const int lo = parts_of(pair_tiles(p, s, 0), c), hi = parts_of(pair_tiles(p, s, pairs - 1), c);
+        if (lo == hi) {
+            t.pairs = pairs * lo;
+        } else {
+            for (int i = 0; i < pairs; ++i)
+                t.pairs += parts_of(pair_tiles(p, s, i), c);
         }
     }
-    float m = -INFINITY, l = 0.f, o0 = 0.f, o1 = 0.f;
-    for (int j0 = 0; j0 < lim; j0 += 32) {
-        const int j = j0 + lane;
-        float s = -INFINITY;
-        int64_t base = -1;
-        if (j < lim) {
-            const int page = p.table[static_cast<int64_t>(b) * p.max_pages + j / p.page_size];
-            if (page < 0 || page >= p.n_pages) {
-                record_bounds_failure(kCheckCachePage);
-            } else {
-                base = page * p.page_stride + hk * p.head_stride + (j % p.page_size) * p.token_stride;
-                s = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint4 x = reinterpret_cast<const uint4 *>(p.k_pages + base)[i];
-                    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        s = fmaf(qv[8 * i + 2 * e], bf16lo_to_f32(xs[e]), s);
-                        s = fmaf(qv[8 * i + 2 * e + 1], bf16hi_to_f32(xs[e]), s);
-                    }
+    if (tiles & 1)
+        t.single = parts_of(key_tiles(p, s, s.n - 1), steps);
+    return t;
+}
+
+// Chooses the largest number of steps of a task and counts the tasks; every
+// CTA of the launch comes to the same.  A candidate cuts the longest range
+// into s parts; its time is taken as the rounds of the CTAs over tasks of
+// that many steps, or, where the tasks are uneven, as the evenly shared work
+// and one task more, whichever is less.
+__device__ __forceinline__ void plan_tasks(CachedSmem &sm, const CachedParams &p)
+{
+    const int tid = threadIdx.x, cap = p.max_splits;
+    if (tid < kMaxSplits)
+        sm.cand_tasks[tid] = 0;
+    if (tid == 0) {
+        sm.longest = 1;
+        sm.work = 0;
+        sm.steps = kNoSplit;
+    }
+    __syncthreads();
+    if (cap > 1) {
+        int longest = 0, work = 0;
+        for (int b = tid; b < p.n_seqs; b += kAttnThreads) {
+            const Seq s = load_seq(p, b);
+            if (s.n == 0)
+                continue;
+            const int tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens, pairs = tiles >> 1;
+            const int kt = key_tiles(p, s, s.n - 1);
+            longest = max(longest, pairs ? 2 * kt : kt);
+            work += tiles * kt;
+        }
+        atomicMax(&sm.longest, longest);
+        atomicAdd(&sm.work, work);
+        __syncthreads();
+        const int total = cap * p.n_seqs;
+        longest = sm.longest;
+        for (int i = tid; i < total; i += kAttnThreads) {
+            const int b = i / cap, c = i - b * cap;
+            const SeqTasks t = seq_tasks(p, load_seq(p, b), (longest + c) / (c + 1));
+            atomicAdd(&sm.cand_tasks[c], t.pairs + t.single);
+        }
+        __syncthreads();
+        if (tid < 32) {
+            const float grid = static_cast<float>(gridDim.x);
+            float best = INFINITY;
+            int at = 0;
+            for (int c = tid; c < cap; c += 32) {
+                const float n = static_cast<float>(sm.cand_tasks[c]) * p.Hkv;
+                const float each = static_cast<float>((longest + c) / (c + 1)) + kTaskOverhead;
+                const float even = (static_cast<float>(sm.work) * p.Hkv + n * kTaskOverhead) / grid + each;
+                const float t = fminf(ceilf(n / grid) * each, even) + (c > 0 ? kJoinOverhead : 0.f);
+                if (t < best) {
+                    best = t;
+                    at = c;
                 }
             }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                const float t = __shfl_xor_sync(0xffffffffu, best, d);
+                const int a = __shfl_xor_sync(0xffffffffu, at, d);
+                if (t < best || (t == best && a < at)) {
+                    best = t;
+                    at = a;
+                }
+            }
+            if (tid == 0) {
+                sm.steps = at > 0 ? (longest + at) / (at + 1) : kNoSplit;
+                if (blockIdx.x == 0)
+                    p.header[0] = sm.steps;
+            }
         }
-        float mx = s;
+        __syncthreads();
+    }
+    // Tasks up to and with every sequence: runs of consecutive sequences per thread.
+    const int steps = sm.steps;
+    const int per = (p.n_seqs + kAttnThreads - 1) / kAttnThreads;
+    const int b0 = min(tid * per, p.n_seqs), b1 = min(b0 + per, p.n_seqs);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        const SeqTasks t = seq_tasks(p, load_seq(p, b), steps);
+        mine += (t.pairs + t.single) * p.Hkv;
+        sm.task_end[b] = mine;
+    }
+    int upto = mine;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const float mn = fmaxf(m, mx), mu = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(m - mu), w = exp2f(s - mu);
-        float sum = w;
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        l = fmaf(l, f, sum);
-        o0 *= f;
-        o1 *= f;
-        m = mn;
-        for (int i = 0; i < 32 && j0 + i < lim; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            const int64_t bi = __shfl_sync(0xffffffffu, base, i);
-            if (bi >= 0) {
-                const uint32_t v = reinterpret_cast<const uint32_t *>(p.v_pages + bi)[lane];
-                o0 = fmaf(wi, bf16lo_to_f32(v), o0);
-                o1 = fmaf(wi, bf16hi_to_f32(v), o1);
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, d);
+        if ((tid & 31) >= d)
+            upto += x;
+    }
+    if ((tid & 31) == 31)
+        sm.scan[tid >> 5] = upto;
+    __syncthreads();
+    for (int w = 0; w < (tid >> 5); ++w)
+        upto += sm.scan[w];
+    for (int b = b0; b < b1; ++b)
+        sm.task_end[b] += upto - mine;
+    if (tid == kAttnThreads - 1)
+        sm.n_tasks = upto;
+    __syncthreads();
+}
+
+__device__ __forceinline__ Task decode_task(const CachedSmem &sm, const CachedParams &p, int i)
+{
+    const int steps = sm.steps, b = upper_bound(sm.task_end, p.n_seqs, i);
+    const int first = b ? sm.task_end[b - 1] : 0, per_head = (sm.task_end[b] - first) / p.Hkv;
+    const Seq s = load_seq(p, b);
+    const int tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens, pairs = tiles >> 1;
+    const int tiles_all = key_tiles(p, s, s.n - 1);
+    const int single = (tiles & 1) ? parts_of(tiles_all, steps) : 0;
+    Task t;
+    t.b = b;
+    t.hk = (i - first) / per_head;
+    int r = i - first - t.hk * per_head, total, most;
+    if (r < per_head - single) {
+        t.pair = 1;
+        most = pair_step_tiles(steps);
+        // The first parts hold every pair; the later ones those whose limit reaches them.
+        const int whole = parts_of(pair_tiles(p, s, 0), most);
+        int pr;
+        if (r < whole * pairs) {
+            t.chunk = r / pairs;
+            pr = r - t.chunk * pairs;
+        } else {
+            r -= whole * pairs;
+            for (t.chunk = whole;; ++t.chunk) {
+                int lo = 0, hi = pairs - 1;  // the last pair reaches every part
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if (pair_tiles(p, s, mid) > t.chunk * most)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                pr = lo + r;
+                if (pr < pairs)
+                    break;
+                r -= pairs - lo;
+            }
+        }
+        total = pair_tiles(p, s, pr);
+        t.row0 = s.row0 + 2 * pr * p.tile_tokens;
+    } else {
+        t.pair = 0;
+        most = steps;
+        t.chunk = r - (per_head - single);
+        total = tiles_all;
+        t.row0 = s.row0 + 2 * pairs * p.tile_tokens;
+    }
+    t.split = total > most;
+    t.kt0 = t.split ? t.chunk * most : 0;
+    t.n = min(total - t.kt0, most);
+    t.row_end = s.row0 + s.n;
+    t.pos0 = s.kv - (t.row_end - t.row0);
+    t.kv = s.kv;
+    t.vlast = min(kBlockN, s.kv - (t.kt0 + t.n - 1) * kBlockN);
+    return t;
+}
+
+// --------------------------------------------------------------- roles
+
+// O = 0 and lse = -inf for the rows of a task none of which sees a key.
+__device__ __forceinline__ void write_empty_rows(const CachedParams &p, int row0, int row_end, int pair, int hk)
+{
+    const int lane = threadIdx.x & 31;
+    const int rows = min(row_end - row0, (pair ? 2 : 1) * p.tile_tokens) * p.group;
+    for (int i = lane >> 3; i < rows; i += 4) {
+        const int tok = i / p.group;
+        const int64_t id = static_cast<int64_t>(row0 + tok) * p.H + hk * p.group + i - tok * p.group;
+        reinterpret_cast<uint4 *>(p.o + id * kHeadDim)[lane & 7] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse && (lane & 7) == 0)
+            p.lse[id] = -INFINITY;
+    }
+}
+
+// Warp 2: the lanes decode 32 tasks at once and hand on, in order, those with
+// keys, then one with n = 0 that ends the list.  Tasks without keys (their
+// sequence was refused pages, e.g.) are dealt with here and never enter the
+// ring: the issuer looks ahead to the next task with keys while it still has
+// products of earlier ones to issue, so it must not have to pass a ring full
+// of empty ones.
+__device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &p, int my_tasks)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t it = 0;
+    for (int base = 0; base <= my_tasks; base += 32) {
+        Task t{};
+        if (base + lane < my_tasks)
+            t = decode_task(sm, p, static_cast<int>(blockIdx.x + (base + lane) * gridDim.x));
+        const int m = min(32, my_tasks + 1 - base);
+        for (int i = 0; i < m; ++i) {
+            if (base + i < my_tasks && __shfl_sync(0xffffffffu, t.n, i) == 0) {
+                write_empty_rows(p, __shfl_sync(0xffffffffu, t.row0, i), __shfl_sync(0xffffffffu, t.row_end, i),
+                                 __shfl_sync(0xffffffffu, t.pair, i), __shfl_sync(0xffffffffu, t.hk, i));
+                continue;
+            }
+            const uint32_t slot = it % kTaskRing;
+            if (!wait_bar_warp(smem_u32(&sm.task_empty[slot]), ((it / kTaskRing) & 1) ^ 1, &sm.ctl, kSiteTaskEmpty))
+                return;
+            if (lane == i) {
+                sm.task[slot] = t;
+                mbar_arrive(smem_u32(&sm.task_full[slot]));
+            }
+            __syncwarp();
+            ++it;
+        }
+    }
+}
+
+// Reads task `it` from the ring (the caller releases it once read).
+__device__ __forceinline__ bool wait_task(CachedSmem &sm, int it)
+{
+    return wait_bar(smem_u32(&sm.task_full[it % kTaskRing]), (static_cast<uint32_t>(it) / kTaskRing) & 1, &sm.ctl,
+                    kSiteTaskFull);
+}
+
+__device__ __forceinline__ void release_task(CachedSmem &sm, int it)
+{
+    mbar_arrive(smem_u32(&sm.task_empty[it % kTaskRing]));
+}
+
+__device__ __forceinline__ void run_cached_producer(CachedSmem &sm, const CUtensorMap *tmQ, const CUtensorMap *tmK,
+                                                    const CUtensorMap *tmV, const CachedParams &p)
+{
+    volatile WaitCtl *ab = &sm.ctl;
+    const int lane = threadIdx.x & 31;
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * kHeadDim * 2;
+    const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * kHeadDim * 2;
+    uint32_t u = 0, k_issued = 0, v_issued = 0, qn = 0;
+    for (int it = 0;; ++it) {
+        const bool got = wait_task(sm, it);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, got))
+            goto out;
+        {
+            const Task &tr = sm.task[it % kTaskRing];
+            const int n = tr.n, hk = tr.hk, pair = tr.pair, row0 = tr.row0, kt0 = tr.kt0, vlast = tr.vlast;
+            const int32_t *table = p.table + static_cast<int64_t>(tr.b) * p.max_pages;
+            __syncwarp();
+            if (lane == 0)
+                release_task(sm, it);
+            if (n == 0)
+                goto out;
+            // Page of this lane's box of tile j; the first key of the box exists.
+            auto lookup = [&](int j) -> int {
+                const int valid = j == n - 1 ? vlast : kBlockN;
+                if (lane * p.box_rows >= valid)
+                    return 0;
+                const int page = __ldg(table + ((kt0 + j) * kBlockN + lane * p.box_rows) / p.page_size);
+                if (page >= 0 && page < p.n_pages)
+                    return page;
+                record_bounds_failure(kCheckCachePage);
+                return p.n_pages;  // outside the map: the box is filled with zeros
+            };
+            int page = lookup(0);
+            const int qb = static_cast<int>(qn & 1);
+            if (!wait_bar_warp(smem_u32(&sm.q_empty[qb]), ((qn >> 1) & 1) ^ 1, ab, kSiteQEmpty))
+                goto out;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(smem_u32(&sm.q_full[qb]), pair ? 2 * q_bytes : q_bytes);
+                tma_load_3d(smem_u32(sm.q[qb][0]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group, row0);
+                if (pair)
+                    tma_load_3d(smem_u32(sm.q[qb][1]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group,
+                                row0 + p.tile_tokens);
+            }
+            ++qn;
+            for (int j = 0; j < n; ++j, ++u) {
+                const int valid = j == n - 1 ? vlast : kBlockN;
+                const int boxes = (valid + p.box_rows - 1) / p.box_rows;
+                const int off = ((kt0 + j) * kBlockN + lane * p.box_rows) % p.page_size;
+                const int here = page;
+                if (j + 1 < n)
+                    page = lookup(j + 1);
+                const uint32_t st = u % kStages, ph = ((u / kStages) & 1) ^ 1;
+                if (!wait_bar_warp(smem_u32(&sm.k_empty[st]), ph, ab, kSiteKEmpty))
+                    goto out;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(smem_u32(&sm.k_full[st]), boxes * box_bytes);
+                ++k_issued;
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_4d(smem_u32(sm.k[st]) + lane * box_bytes, tmK, smem_u32(&sm.k_full[st]), 0, off, hk, here);
+                if (!wait_bar_warp(smem_u32(&sm.v_empty[st]), ph, ab, kSiteVEmpty))
+                    goto out;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(smem_u32(&sm.v_full[st]), boxes * box_bytes);
+                ++v_issued;
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_4d(smem_u32(sm.v[st]) + lane * box_bytes, tmV, smem_u32(&sm.v_full[st]), 0, off, hk, here);
             }
         }
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+out:
+    // Every copy this warp started must land before the CTA may exit.
+    __syncwarp();
+    if (lane == 0) {
+        for (uint32_t i = (k_issued > kStages ? k_issued - kStages : 0); i < k_issued; ++i)
+            wait_drain(smem_u32(&sm.k_full[i % kStages]), (i / kStages) & 1);
+        for (uint32_t i = (v_issued > kStages ? v_issued - kStages : 0); i < v_issued; ++i)
+            wait_drain(smem_u32(&sm.v_full[i % kStages]), (i / kStages) & 1);
+        for (uint32_t i = (qn > 2 ? qn - 2 : 0); i < qn; ++i)
+            wait_drain(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1);
+    }
+    __syncwarp();
+}
+
+// Position of the issuer in the steps of this CTA's tasks.  Within a task
+// step s belongs to warpgroup s & 1, and to key tile s / 2 (pair) or s (single).
+struct TaskCursor {
+    int it, s, steps;   // task, step within it, its steps (0: before the first task)
+    int pair, kk_last;  // PV products of 16 keys in its last key tile
+    uint32_t st, ph;    // K/V ring stage and its phase
+    uint32_t buf;       // score buffer
+    uint32_t c0, c1;    // steps of each warpgroup so far
+
+    // Reads task `it`; false at the end of the tasks or when the wait ran out.
+    template <bool kRelease>
+    __device__ __forceinline__ bool open(CachedSmem &sm)
+    {
+        if (!wait_task(sm, it))
+            return false;
+        const Task &t = sm.task[it % kTaskRing];
+        const int n = t.n;
+        pair = t.pair;
+        kk_last = (t.vlast + 15) >> 4;
+        if (kRelease)
+            release_task(sm, it);
+        steps = pair ? 2 * n : n;
+        s = 0;
+        return n > 0;
+    }
+
+    __device__ __forceinline__ uint32_t wg() const { return static_cast<uint32_t>(s) & 1u; }
+    __device__ __forceinline__ uint32_t count() const { return wg() ? c1 : c0; }
+    __device__ __forceinline__ bool last_reader() const { return !pair || wg(); }
+    __device__ __forceinline__ bool first_reader() const { return !pair || !wg(); }
+
+    template <bool kRelease>
+    __device__ __forceinline__ bool next(CachedSmem &sm)
+    {
+        if (last_reader() && ++st == kStages) {
+            st = 0;
+            ph ^= 1u;
+        }
+        if (wg())
+            ++c1;
+        else
+            ++c0;
+        buf = buf == kScoreBufs - 1 ? 0u : buf + 1;
+        if (++s < steps)
+            return true;
+        ++it;
+        return open<kRelease>(sm);
+    }
+};
+
+__device__ __forceinline__ void issue_score(CachedSmem &sm, uint32_t tmem, const TaskCursor &c, const TileDescs &td)
+{
+    constexpr uint32_t kIdescS = idesc_bf16_f32(kBlockM, kBlockN, false);
+    const uint32_t qb = static_cast<uint32_t>(c.it) & 1u;
+    const uint64_t a = td.q0 + (2 * qb + (c.pair ? c.wg() : 0u)) * kTileDescStep, b = td.k0 + c.st * kTileDescStep;
+    const uint32_t d = tmem + c.buf * kBlockN;
+#pragma unroll
+    for (int kk = 0; kk < kHeadDim / 16; ++kk)
+        umma_ss(d, a + 2 * kk, b + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
+    umma_commit(smem_u32(&sm.s_full[c.wg()][c.count() % 3]));
+    if (c.last_reader())
+        umma_commit(smem_u32(&sm.k_empty[c.st]));
+    if (c.s == c.steps - 1)
+        umma_commit(smem_u32(&sm.q_empty[qb]));
+}
+
+__device__ __forceinline__ bool score_ready(CachedSmem &sm, const TaskCursor &c)
+{
+    if (c.s == 0 && !wait_bar(smem_u32(&sm.q_full[static_cast<uint32_t>(c.it) & 1u]), (static_cast<uint32_t>(c.it) >> 1) & 1u, &sm.ctl, kSiteQFull))
+        return false;
+    return !c.first_reader() || wait_bar(smem_u32(&sm.k_full[c.st]), c.ph, &sm.ctl, kSiteKFull);
+}
+
+__device__ __forceinline__ void cached_mma_loop(CachedSmem &sm, uint32_t tmem)
+{
+    constexpr uint32_t kIdescPV = idesc_bf16_f32(kBlockM, kHeadDim, true);
+    volatile WaitCtl *ab = &sm.ctl;
+    const TileDescs td{sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024), sdesc_sw128(smem_u32(sm.k[0]), 16, 1024),
+                       sdesc_sw128(smem_u32(sm.v[0]), 16, 1024)};
+    TaskCursor sc{}, vc{};  // next S, next PV to issue
+    bool s_more = sc.open<false>(sm);
+    bool v_more = vc.open<true>(sm);
+    for (int i = 0; i < kScoreBufs && s_more; ++i) {
+        if (!score_ready(sm, sc))
+            return;
+        tc_fence_after();
+        issue_score(sm, tmem, sc, td);
+        s_more = sc.next<false>(sm);
+    }
+    while (v_more) {
+        const uint32_t wg = vc.wg(), c = vc.count();
+        if (vc.first_reader() && !wait_bar(smem_u32(&sm.v_full[vc.st]), vc.ph, ab, kSiteVFull))
+            return;
+        if (!wait_bar(smem_u32(&sm.p_ready[wg][c % 3]), (c / 3) & 1u, ab, kSitePReady))
+            return;
+        tc_fence_after();
+        const uint64_t b = td.v0 + vc.st * kTileDescStep;
+        const uint32_t d = tmem + kTmemO + wg * kHeadDim, a = tmem + vc.buf * kBlockN;
+        const bool last = vc.pair ? vc.s >= vc.steps - 2 : vc.s == vc.steps - 1;  // the task's last key tile
+        const int kks = last ? vc.kk_last : kBlockN / 16;
+#pragma unroll
+        for (int kk = 0; kk < kBlockN / 16; ++kk)
+            if (kk < kks)
+                umma_ts(d, a + 8 * kk, b + 128 * kk, kIdescPV, (vc.s >= 2 || kk > 0) ? 1u : 0u);
+        umma_commit(smem_u32(&sm.o_done[wg]));
+        if (vc.s >= vc.steps - 2)  // the warpgroup's last step of the task
+            umma_commit(smem_u32(&sm.o_final[wg]));
+        if (vc.last_reader())
+            umma_commit(smem_u32(&sm.v_empty[vc.st]));
+        v_more = vc.next<true>(sm);
+        if (s_more) {
+            // S(k + 3) overwrites the buffer PV(k) reads P from.
+            if (!score_ready(sm, sc))
+                return;
+            if (!wait_bar(smem_u32(&sm.o_done[wg]), c & 1u, ab, kSiteODone))
+                return;
+            tc_fence_after();
+            issue_score(sm, tmem, sc, td);
+            s_more = sc.next<false>(sm);
+        }
+    }
+}
+
+__device__ __forceinline__ void run_cached_mma(CachedSmem &sm, uint32_t tmem)
+{
+    if (elect_one()) {
+        cached_mma_loop(sm, tmem);
+        // Every UMMA issued must complete before TMEM is released.
+        umma_commit(smem_u32(&sm.drain));
+        wait_drain(smem_u32(&sm.drain), 0);
+    }
+    __syncwarp();
+}
+
+// One row's result: O (columns of tO, and of tO1 for a merged single tile,
+// weighted w0 and w1) with the row's l and m.
+__device__ __forceinline__ void finish_cached_row(const CachedParams &p, uint32_t tO, uint32_t tO1, bool merged,
+                                                  float w0, float w1, const Task &t, int row, int h, bool row_ok,
+                                                  float l, float m)
+{
+    const int64_t id = static_cast<int64_t>(row) * p.H + h;
+    const bool go = row_ok && VGGT_IN_RANGE(row >= 0 && row < p.n_rows && h < p.H && t.chunk < p.max_splits,
+                                            kCheckAttnRow);
+    const float f = t.split ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+    const float f0 = merged ? w0 * f : f, f1 = w1 * f;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        uint32_t o[32];
+        float v[32];
+        tmem_ld32(tO + 32 * half, o);
+        tmem_ld_wait();
+        reg_fence(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            v[e] = __uint_as_float(o[e]) * f0;
+        if (merged) {
+            tmem_ld32(tO1 + 32 * half, o);
+            tmem_ld_wait();
+            reg_fence(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                v[e] = fmaf(__uint_as_float(o[e]), f1, v[e]);
+        }
+        if (!go)
+            continue;
+        if (t.split) {
+            float4 *dst = reinterpret_cast<float4 *>(
+                p.part_o + ((static_cast<int64_t>(t.chunk) * p.n_rows * p.H) + id) * kHeadDim + 32 * half);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
+            uint4 *dst = reinterpret_cast<uint4 *>(p.o + id * kHeadDim + 32 * half);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                dst[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                    pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+        }
+    }
+    if (!go)
+        return;
+    if (t.split)
+        p.part_ml[static_cast<int64_t>(t.chunk) * p.n_rows * p.H + id] = make_float2(m, l);
+    else if (p.lse)
+        p.lse[id] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+}
+
+__device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem, const CachedParams &p, int wg)
+{
+    volatile WaitCtl *ab = &sm.ctl;
+    const int t = static_cast<int>(threadIdx.x) - kBlockM * (wg + 1);  // row within the tile
+    const uint32_t lane_off = static_cast<uint32_t>((t >> 5) * 32) << 16;
+    const uint32_t tO = tmem + kTmemO + static_cast<uint32_t>(wg * kHeadDim) + lane_off;
+    const uint32_t bar_s = smem_u32(&sm.s_full[wg][0]), bar_p = smem_u32(&sm.p_ready[wg][0]);
+    const uint32_t bar_o = smem_u32(&sm.o_done[wg]), bar_of = smem_u32(&sm.o_final[wg]);
+    const float sl2 = p.scale_log2;
+    const uint64_t sl2_2 = f2_pack(sl2, sl2);
+    const uint64_t magic2 = f2_pack(kRoundMagic, kRoundMagic);
+    const uint64_t neg_magic2 = f2_pack(-kRoundMagic, -kRoundMagic);
+    const uint64_t neg_one2 = f2_pack(-1.f, -1.f);
+    const uint64_t c0_2 = f2_pack(kExp2C0, kExp2C0), c1_2 = f2_pack(kExp2C1, kExp2C1);
+    const uint64_t c2_2 = f2_pack(kExp2C2, kExp2C2), c3_2 = f2_pack(kExp2C3, kExp2C3);
+    const int tok = t / p.group, tile_head = t - tok * p.group;
+    uint32_t k0 = 0;         // steps of the CTA before the task
+    uint32_t ring = 0;       // key tiles before the task
+    uint32_t c = 0;          // steps of this warpgroup
+    uint32_t finals = 0;     // tasks in which it had a step
+    uint32_t merges = 0;     // single-tile tasks that both warpgroups worked on
+    bool merge_open = false; // warpgroup 1: its last merge has not been read yet
+
+    for (int it = 0;; ++it) {
+        const bool got = wait_task(sm, it);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, got))
+            return;
+        const Task w = sm.task[it % kTaskRing];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            release_task(sm, it);
+        if (w.n == 0)
+            return;
+        const int tile_tok = (w.pair && wg ? p.tile_tokens : 0) + tok;  // token within the task
+        const int row = w.row0 + tile_tok;
+        const bool row_ok = tok < p.tile_tokens && row < w.row_end;
+        const int head = w.hk * p.group + tile_head;
+        const int steps = w.pair ? w.n : (w.n + 1 - wg) >> 1;  // of this warpgroup
+        // keys this row sees, counted from the task's first key
+        const int lim = row_ok ? key_limit(w.kv, w.pos0 + tile_tok, p.unit) - w.kt0 * kBlockN : 0;
+        const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+        const int warp_lim = __reduce_min_sync(0xffffffffu, row_ok ? lim : 0x7fffffff);
+        float m = -INFINITY, l = 0.f;
+
+        for (int x = 0; x < steps; ++x, ++c) {
+            const int j = w.pair ? x : 2 * x + wg;  // key tile within the task
+            const uint32_t buf = (k0 + static_cast<uint32_t>(2 * x + wg)) % kScoreBufs;
+            const uint32_t tS = tmem + buf * kBlockN + lane_off;
+            if (!wait_bar_warp(bar_s + 8 * (c % 3), (c / 3) & 1, ab, kSiteSFull))
+                return;
+            if (j == w.n - 1 && (w.vlast & 15) != 0 && (!w.pair || wg == 0)) {
+                // V rows behind the last key, up to the end of its group of 16
+                const uint32_t u = ring + static_cast<uint32_t>(j), st = u % kStages;
+                if (!wait_bar_warp(smem_u32(&sm.v_full[st]), (u / kStages) & 1, ab, kSiteVFull))
+                    return;
+                const int r = w.vlast + (t >> 3);
+                if (r < ((w.vlast + 15) & ~15))
+                    reinterpret_cast<uint4 *>(sm.v[st] + r * kHeadDim * 2)[t & 7] = make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+            }
+            if (warp_ok) {
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    tmem_ld32(tS + 32 * i, s[i]);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    reg_fence(s[i]);
+                const int valid = lim - j * kBlockN;
+                if (warp_lim < (j + 1) * kBlockN) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * i + e >= valid)
+                                s[i][e] = __float_as_uint(-INFINITY);
+                }
+                // Row max of the tile, in log2 units.
+                auto tile_max = [&]() -> float {
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mx[i] = fmax3(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]), __uint_as_float(s[i][2]));
+#pragma unroll
+                        for (int e = 3; e < 31; e += 2)
+                            mx[i] = fmax3(mx[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+                        mx[i] = fmaxf(mx[i], __uint_as_float(s[i][31]));
+                    }
+                    return fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * sl2;
+                };
+                // P = 2^(s*scale*log2e - m) as bf16 pairs over the first 64
+                // columns of the score buffer; returns the fp32 sum of P
+                // before it is rounded (see attn_fwd_kernel for the split of
+                // the exponentials between the MUFU unit and a polynomial).
+                auto exp_tile = [&]() -> float {
+                    const float base = m == -INFINITY ? 0.f : m;  // a row that sees nothing: P = 0
+                    const uint64_t neg_m2 = f2_pack(-base, -base);
+                    uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint64_t x2 = f2_fma(
+                                f2_pack(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), sl2_2, neg_m2);
+                            float a, b;
+                            f2_unpack(x2, a, b);
+                            if (e < kExp2PolyPairs) {
+                                const uint64_t xc = f2_pack(fmaxf(a, kExp2MinArg), fmaxf(b, kExp2MinArg));
+                                const uint64_t y = f2_add(xc, magic2);
+                                const uint64_t jj = f2_add(y, neg_magic2);
+                                const uint64_t f = f2_fma(jj, neg_one2, xc);
+                                uint64_t q = f2_fma(c3_2, f, c2_2);
+                                q = f2_fma(q, f, c1_2);
+                                q = f2_fma(q, f, c0_2);
+                                float qa, qb, ya, yb;
+                                f2_unpack(q, qa, qb);
+                                f2_unpack(y, ya, yb);
+                                a = __uint_as_float(__float_as_uint(ya) * 8388608u + __float_as_uint(qa));
+                                b = __uint_as_float(__float_as_uint(yb) * 8388608u + __float_as_uint(qb));
+                            } else {
+                                a = ex2_approx(a);
+                                b = ex2_approx(b);
+                            }
+                            ls[e & 3] = f2_add(ls[e & 3], f2_pack(a, b));
+                            pk[e] = pack_bf16x2(a, b);
+                        }
+                        tmem_st16(tS + 16 * i, pk);
+                    }
+                    const uint64_t t2 = f2_add(f2_add(ls[0], ls[1]), f2_add(ls[2], ls[3]));
+                    float ta, tb;
+                    f2_unpack(t2, ta, tb);
+                    return ta + tb;
+                };
+                // Lazy offset, as in attn_fwd_kernel: the first tile sets m,
+                // and a later tile whose row sum passes kTileSumLimit takes
+                // the exact path.
+                if (x == 0)
+                    m = tile_max();
+                float tsum = exp_tile();
+                if (x > 0 && __any_sync(0xffffffffu, !(tsum <= kTileSumLimit))) {
+                    const float cand = tile_max();
+                    const bool need = cand > m + kRescaleThreshold;
+                    if (__any_sync(0xffffffffu, need)) {
+                        if (!wait_bar_warp(bar_o, (c - 1) & 1, ab, kSiteODone))
+                            return;
+                        tc_fence_after();
+                        const float f = need ? ex2_approx(m - cand) : 1.f;
+#pragma unroll 1
+                        for (int quarter = 0; quarter < 4; ++quarter) {
+                            uint32_t o[16];
+                            tmem_ld16(tO + 16 * quarter, o);
+                            tmem_ld_wait();
+                            reg_fence(o);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(tO + 16 * quarter, o);
+                        }
+                        tmem_st_wait();
+                        if (need) {
+                            l *= f;
+                            m = cand;
+                        }
+                    }
+                    tmem_st_wait();  // the first pass's P stores land before they are overwritten
+                    tsum = exp_tile();
+                }
+                l += tsum;
+                tmem_st_wait();
+            }
+            if (merge_open) {
+                // warpgroup 0 still reads this warpgroup's O of an earlier task
+                if (!wait_bar_warp(smem_u32(&sm.merge_free), (merges - 1) & 1, ab, kSiteMergeFree))
+                    return;
+                merge_open = false;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0)
+                mbar_arrive(bar_p + 8 * (c % 3));
+        }
+        k0 += static_cast<uint32_t>(w.pair ? 2 * w.n : w.n);
+        ring += static_cast<uint32_t>(w.n);
+
+        if (steps == 0)
+            continue;  // a single tile of one step: warpgroup 0's alone
+        if (!wait_bar_warp(bar_of, finals & 1, ab, kSiteOFinal))
+            return;
+        ++finals;
+        tc_fence_after();
+        const bool merged = !w.pair && w.n > 1;
+        if (merged && wg == 1) {
+            if (merge_open && !wait_bar_warp(smem_u32(&sm.merge_free), (merges - 1) & 1, ab, kSiteMergeFree))
+                return;
+            sm.merge_ml[t] = make_float2(m, l);
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0)
+                mbar_arrive(smem_u32(&sm.merge_ready));
+            ++merges;
+            merge_open = true;
+            continue;
+        }
+        float w0 = 1.f, w1 = 0.f;
+        if (merged) {
+            if (!wait_bar_warp(smem_u32(&sm.merge_ready), merges & 1, ab, kSiteMergeReady))
+                return;
+            ++merges;
+            tc_fence_after();
+            const float2 ml = sm.merge_ml[t];
+            // A part without keys has l = 0 and m = -inf: it gets weight 0.  NaN passes through.
+            const float top = fmaxf(m, ml.x);
+            w0 = m == -INFINITY ? 0.f : ex2_approx(m - top);
+            w1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+            l = l * w0 + ml.y * w1;
+            m = top;
+        }
+        if (m == -INFINITY)
+            l = 0.f;  // the row sees no key of the task; masked columns may have left 2^-125 each
+        if (warp_ok)
+            finish_cached_row(p, tO, tO + kHeadDim, merged, w0, w1, w, row, head, row_ok, l, m);
+        tc_fence_before();
+        if (merged) {
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0)
+                mbar_arrive(smem_u32(&sm.merge_free));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    cached_attn_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                       const __grid_constant__ CUtensorMap tmV, const CachedParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    CachedSmem &sm = *reinterpret_cast<CachedSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                     ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // The joining launch may be set up; it waits for this one before it reads.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.q_full[i]), 1);
+            mbar_init(smem_u32(&sm.q_empty[i]), 1);
+            for (int c = 0; c < 3; ++c) {
+                mbar_init(smem_u32(&sm.s_full[i][c]), 1);
+                mbar_init(smem_u32(&sm.p_ready[i][c]), 4);
+            }
+            mbar_init(smem_u32(&sm.o_done[i]), 1);
+            mbar_init(smem_u32(&sm.o_final[i]), 1);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sm.k_full[i]), 1);
+            mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v_full[i]), 1);
+            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+        }
+        for (int i = 0; i < kTaskRing; ++i) {
+            mbar_init(smem_u32(&sm.task_full[i]), 1);
+            mbar_init(smem_u32(&sm.task_empty[i]), 10);  // producer, issuer, eight softmax warps
+        }
+        mbar_init(smem_u32(&sm.merge_ready), 4);
+        mbar_init(smem_u32(&sm.merge_free), 4);
+        mbar_init(smem_u32(&sm.drain), 1);
+        sm.ctl.abort = 0;
+        sm.ctl.limit_ns = p.wait_limit_ns;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    plan_tasks(sm, p);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    const int n_tasks = sm.n_tasks, cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
+    const int my_tasks = n_tasks > cta ? (n_tasks - cta + ctas - 1) / ctas : 0;
+
+    // 168 registers/thread at launch; 128 x (72 + 216 + 216) = 384 x 168.
+    if (warp < 4) {
+        setmaxnreg_dec<kRegsControl>();
+        if (warp == 0)
+            run_cached_producer(sm, &tmQ, &tmK, &tmV, p);
+        else if (warp == 1)
+            run_cached_mma(sm, tmem);
+        else if (warp == 2)
+            run_decoder(sm, p, my_tasks);
+    } else {
+        setmaxnreg_inc<kRegsSoftmax>();
+        run_cached_softmax(sm, tmem, p, (warp >> 2) - 1);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the parts of the rows whose keys were cut: O = sum_c 2^{m_c - M} O_c /
+// sum_c 2^{m_c - M} l_c, M = max m_c, in the order of the parts.  One warp per
+// row and head, two channels per lane.  Bound by latency and the parts' bytes.
+__global__ void __launch_bounds__(256) cached_combine_kernel(const CachedParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t rows = static_cast<int64_t>(p.n_rows) * p.H;
+    int row = static_cast<int>(id / p.H), b = 0, parts = 1;
+    Seq s{0, 0, 0};
+    bool live = id < rows;
+    if (live) {
+        // The sequence of the row: the lanes look at 32 offsets at a time.
+        int lo = 0, hi = p.n_seqs;  // cu_rows[lo] <= row < cu_rows[hi], if row has a sequence
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, at = min(lo + (lane + 1) * step, hi);
+            const unsigned over = __ballot_sync(0xffffffffu, at >= hi || __ldg(p.cu_rows + at) > row);
+            const int first = __ffs(over) - 1;  // at least lane 31's is over
+            hi = min(lo + (first + 1) * step, hi);
+            lo += first * step;
+        }
+        b = lo;
+        s = load_seq(p, b);
+        live = row >= s.row0 && row < s.row0 + s.n;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!live)
+        return;
+    const int steps = p.header[0];
+    if (steps == kNoSplit)
+        return;
+    const int tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens, tile = (row - s.row0) / p.tile_tokens;
+    if (tile < (tiles & ~1))
+        parts = parts_of(pair_tiles(p, s, tile >> 1), pair_step_tiles(steps));
+    else
+        parts = parts_of(key_tiles(p, s, s.n - 1), steps);
+    if (parts == 1)
+        return;  // written whole
+    float m[kMaxSplits / 32], l[kMaxSplits / 32], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / 32; ++i) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane + 32 * i < parts)
+            ml = p.part_ml[(lane + 32 * i) * rows + id];
+        m[i] = ml.x;
+        l[i] = ml.y;
+        top = fmaxf(top, ml.x);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / 32; ++i) {
+        m[i] = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - top);  // now the part's weight
+        sum = fmaf(m[i], l[i], sum);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    float o0 = 0.f, o1 = 0.f;
+    const float2 *src = reinterpret_cast<const float2 *>(p.part_o) + id * (kHeadDim / 2) + lane;
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / 32; ++i) {
+        const int here = min(32, parts - 32 * i);
+#pragma unroll 4
+        for (int c = 0; c < here; ++c) {
+            const float w = __shfl_sync(0xffffffffu, m[i], c);
+            const float2 v = src[(32 * i + c) * rows * (kHeadDim / 2)];
+            o0 = fmaf(w, v.x, o0);
+            o1 = fmaf(w, v.y, o1);
+        }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     reinterpret_cast<uint32_t *>(p.o + id * kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
     if (p.lse && lane == 0)
-        p.lse[id] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : (l == 0.f ? -INFINITY : l);
+        p.lse[id] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
 }
 
 } // namespace vggt

@@ -204,6 +204,44 @@ CachedLayout cached_layout(const vggt_cache &c, int64_t n_rows, int cap)
     return l;
 }
 
+// Query rows [n_rows, H, 64] with their strides; a box holds the G heads of
+// one key head for F tokens.
+bool make_query_map(CUtensorMap *map, const void *q, const vggt_cache &c, int64_t n_rows, int64_t row_stride,
+                    int64_t head_stride, int group, int tokens)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(vggt::kHeadDim), static_cast<cuuint64_t>(c.n_heads),
+                                static_cast<cuuint64_t>(n_rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(row_stride) * 2};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(vggt::kHeadDim), static_cast<cuuint32_t>(group),
+                               static_cast<cuuint32_t>(tokens)};
+    const cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Pages as (64, page_size, n_kv_heads, n_pages); a box is box_rows positions
+// of one head of one page.
+bool make_pages_map(CUtensorMap *map, const void *pages, const vggt_cache &c, int box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(vggt::kHeadDim), static_cast<cuuint64_t>(c.page_size),
+                                static_cast<cuuint64_t>(c.n_kv_heads), static_cast<cuuint64_t>(c.n_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(c.token_stride) * 2,
+                                   static_cast<cuuint64_t>(c.head_stride) * 2,
+                                   static_cast<cuuint64_t>(c.page_stride) * 2};
+    const cuuint32_t box[4] = {static_cast<cuuint32_t>(vggt::kHeadDim), static_cast<cuuint32_t>(box_rows), 1u, 1u};
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pages), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 } // namespace
 
 VGGT_API size_t vggt_attn_cached_workspace_bytes(vggt_cache cache, int32_t n_rows)
@@ -254,35 +292,62 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
             if (out_bytes[i] > 0 && out_bytes[j] > 0 && overlaps(out[i], out_bytes[i], out[j], out_bytes[j]))
                 return VGGT_ERR_INVALID_ARG;
     }
+    int num_sms = 0;
+    if ((st = prepare_device(num_sms)) != VGGT_OK)
+        return st;
     vggt::CachedParams p;
     std::memset(&p, 0, sizeof p);
     p.n_seqs = cache.n_seqs;
     p.n_rows = n_rows;
     p.H = cache.n_heads;
     p.Hkv = cache.n_kv_heads;
+    p.group = cache.n_heads / cache.n_kv_heads;
+    p.tile_tokens = vggt::kBlockM / p.group;
     p.page_size = cache.page_size;
     p.n_pages = cache.n_pages;
     p.max_pages = cache.max_pages;
     p.unit = causal_unit;
+    p.box_rows = cache.page_size & -cache.page_size;
+    if (p.box_rows > vggt::kBlockN)
+        p.box_rows = vggt::kBlockN;
+    p.max_splits = need > 0 ? split_cap(cache, n_rows) : 1;
     p.scale_log2 = scale * 1.4426950408889634f;
-    p.q_row_stride = q_row_stride;
-    p.q_head_stride = q_head_stride;
-    p.page_stride = cache.page_stride;
-    p.head_stride = cache.head_stride;
-    p.token_stride = cache.token_stride;
-    p.q = static_cast<const __nv_bfloat16 *>(q);
-    p.k_pages = static_cast<const __nv_bfloat16 *>(k_pages);
-    p.v_pages = static_cast<const __nv_bfloat16 *>(v_pages);
     p.table = block_table;
     p.cu_rows = cu_rows;
     p.kv_lens = kv_lens;
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.lse = lse;
-    const int64_t blocks = (static_cast<int64_t>(n_rows) * cache.n_heads + 3) / 4;
-    if (blocks > INT32_MAX)
-        return VGGT_ERR_UNSUPPORTED;
-    vggt::cached_attn_kernel<<<static_cast<unsigned>(blocks), 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    return launched();
+    p.wait_limit_ns = vggt::kWaitLimitNs;
+    if (need > 0) {
+        const CachedLayout l = cached_layout(cache, n_rows, p.max_splits);
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        p.header = reinterpret_cast<int32_t *>(ws);
+        p.part_ml = reinterpret_cast<float2 *>(ws + l.ml);
+        p.part_o = reinterpret_cast<float *>(ws + l.po);
+    }
+    CUtensorMap tq, tk, tv;
+    if (!make_query_map(&tq, q, cache, n_rows, q_row_stride, q_head_stride, p.group, p.tile_tokens) ||
+        !make_pages_map(&tk, k_pages, cache, p.box_rows) || !make_pages_map(&tv, v_pages, cache, p.box_rows))
+        return VGGT_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    vggt::cached_attn_kernel<<<num_sms, vggt::kAttnThreads, vggt::cached_smem_bytes(cache.n_seqs), s>>>(tq, tk, tv, p);
+    if ((st = launched()) != VGGT_OK || p.max_splits == 1)
+        return st;
+    // The joining launch is set up while the attention runs and waits for its
+    // end on the device.
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, vggt::cached_combine_kernel, p) != cudaSuccess)
+        return VGGT_ERR_CUDA;
+    return VGGT_OK;
 }
 
 namespace {

@@ -270,7 +270,9 @@ vggt_status prepare_device(int &num_sms)
         if (cudaFuncSetAttribute(vggt::attn_fwd_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(vggt::kAttnSmemBytes)) != cudaSuccess ||
             cudaFuncSetAttribute(vggt::attn_fwd_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(vggt::kAttnSmemBytes)) != cudaSuccess)
+                                 static_cast<int>(vggt::kAttnSmemBytes)) != cudaSuccess ||
+            cudaFuncSetAttribute(vggt::cached_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(vggt::cached_smem_bytes(vggt::kCacheMaxSeqs))) != cudaSuccess)
             return VGGT_ERR_CUDA;
         g_attr_done[dev] = true;
     }
