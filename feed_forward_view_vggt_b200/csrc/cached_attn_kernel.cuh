@@ -56,7 +56,11 @@ constexpr int kNoSplit = 0x7fffffff;
 // joining launch, in steps: used to choose `steps` only.
 constexpr float kTaskOverhead = 4.f, kJoinOverhead = 4.f;
 
-enum : uint32_t { kSiteTaskFull = 12, kSiteTaskEmpty, kSiteMergeReady, kSiteMergeFree };
+constexpr int kFewRows = 16;      // rows of a task that the warps work on by themselves
+constexpr int kSoftmaxWarps = 8;  // and with how many: 16 keys of a tile each
+
+enum : uint32_t { kSiteTaskFull = 12, kSiteTaskEmpty, kSiteMergeReady, kSiteMergeFree, kSiteFewQ, kSiteFewFull, kSiteTaskPassed };
+enum : int { kTaskSingle = 0, kTaskPair = 1, kTaskFew = 2 };
 
 struct CachedParams {
     int n_seqs, n_rows, H, Hkv, group, tile_tokens;  // group G = H / Hkv, tile_tokens F
@@ -77,7 +81,7 @@ struct Task {
     int pos0, kv;       // position of row0's token, keys of the sequence
     int kt0, n;         // first key tile, key tiles (0: the end of the CTA's tasks)
     int b, hk;
-    int pair, split, chunk;
+    int kind, split, chunk;
     int vlast;          // keys of the last tile that exist, 1..128
 };
 
@@ -86,13 +90,15 @@ struct __align__(1024) CachedSmem {
     uint8_t k[kStages][kTileBytes];
     uint8_t v[kStages][kTileBytes];
     Task task[kTaskRing];
-    float2 merge_ml[kBlockM];
+    float2 merge_ml[kBlockM];  // warpgroup 1's (m, l) of a single tile; [warp][row] of a task of few rows
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[kStages], k_empty[kStages];
     uint64_t v_full[kStages], v_empty[kStages];
     uint64_t s_full[2][3], p_ready[2][3];  // by warpgroup and its step count mod 3
     uint64_t o_done[2], o_final[2];
     uint64_t merge_ready, merge_free;
+    uint64_t few_q, few_full[2];  // by tasks of few rows mod 2
+    uint64_t task_passed[2 * kTaskRing];  // the issuer has done with the task
     uint64_t task_full[kTaskRing], task_empty[kTaskRing];
     uint64_t drain;
     uint32_t tmem_base;
@@ -292,7 +298,7 @@ __device__ __forceinline__ Task decode_task(const CachedSmem &sm, const CachedPa
     t.hk = (i - first) / per_head;
     int r = i - first - t.hk * per_head, total, most;
     if (r < per_head - single) {
-        t.pair = 1;
+        t.kind = kTaskPair;
         most = pair_step_tiles(steps);
         // The first parts hold every pair; the later ones those whose limit reaches them.
         const int whole = parts_of(pair_tiles(p, s, 0), most);
@@ -320,7 +326,7 @@ __device__ __forceinline__ Task decode_task(const CachedSmem &sm, const CachedPa
         total = pair_tiles(p, s, pr);
         t.row0 = s.row0 + 2 * pr * p.tile_tokens;
     } else {
-        t.pair = 0;
+        t.kind = (s.n - 2 * pairs * p.tile_tokens) * p.group <= kFewRows ? kTaskFew : kTaskSingle;
         most = steps;
         t.chunk = r - (per_head - single);
         total = tiles_all;
@@ -339,10 +345,10 @@ __device__ __forceinline__ Task decode_task(const CachedSmem &sm, const CachedPa
 // --------------------------------------------------------------- roles
 
 // O = 0 and lse = -inf for the rows of a task none of which sees a key.
-__device__ __forceinline__ void write_empty_rows(const CachedParams &p, int row0, int row_end, int pair, int hk)
+__device__ __forceinline__ void write_empty_rows(const CachedParams &p, int row0, int row_end, int kind, int hk)
 {
     const int lane = threadIdx.x & 31;
-    const int rows = min(row_end - row0, (pair ? 2 : 1) * p.tile_tokens) * p.group;
+    const int rows = min(row_end - row0, (kind == kTaskPair ? 2 : 1) * p.tile_tokens) * p.group;
     for (int i = lane >> 3; i < rows; i += 4) {
         const int tok = i / p.group;
         const int64_t id = static_cast<int64_t>(row0 + tok) * p.H + hk * p.group + i - tok * p.group;
@@ -370,7 +376,7 @@ __device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &
         for (int i = 0; i < m; ++i) {
             if (base + i < my_tasks && __shfl_sync(0xffffffffu, t.n, i) == 0) {
                 write_empty_rows(p, __shfl_sync(0xffffffffu, t.row0, i), __shfl_sync(0xffffffffu, t.row_end, i),
-                                 __shfl_sync(0xffffffffu, t.pair, i), __shfl_sync(0xffffffffu, t.hk, i));
+                                 __shfl_sync(0xffffffffu, t.kind, i), __shfl_sync(0xffffffffu, t.hk, i));
                 continue;
             }
             const uint32_t slot = it % kTaskRing;
@@ -413,7 +419,8 @@ __device__ __forceinline__ void run_cached_producer(CachedSmem &sm, const CUtens
             goto out;
         {
             const Task &tr = sm.task[it % kTaskRing];
-            const int n = tr.n, hk = tr.hk, pair = tr.pair, row0 = tr.row0, kt0 = tr.kt0, vlast = tr.vlast;
+            const int n = tr.n, hk = tr.hk, row0 = tr.row0, kt0 = tr.kt0, vlast = tr.vlast;
+            const bool pair = tr.kind == kTaskPair;
             const int32_t *table = p.table + static_cast<int64_t>(tr.b) * p.max_pages;
             __syncwarp();
             if (lane == 0)
@@ -484,37 +491,78 @@ out:
     __syncwarp();
 }
 
+// The issuer has left task `it` behind; for one of few rows this means that
+// all products of the tasks before it are complete.  The warps wait for that
+// before they follow the K/V ring themselves: a warp that had no step in some
+// single tiles would otherwise take an older phase of a ring barrier for the
+// one it waits for (as would an issuer that is ahead of the warps, see fews_over).  Twice the slots of the task ring keep the phases of
+// these barriers apart: the issuer has left task it - 16 when task it appears
+// in the ring, and cannot reach task it + 16 before the warps release task it + 8.
+__device__ __forceinline__ void pass_task(CachedSmem &sm, int it)
+{
+    mbar_arrive(smem_u32(&sm.task_passed[it % (2 * kTaskRing)]));
+}
+
 // Position of the issuer in the steps of this CTA's tasks.  Within a task
 // step s belongs to warpgroup s & 1, and to key tile s / 2 (pair) or s (single).
 struct TaskCursor {
-    int it, s, steps;   // task, step within it, its steps (0: before the first task)
-    int pair, kk_last;  // PV products of 16 keys in its last key tile
+    int it, s, steps;   // task, step within it, its steps
+    int kind;           // of the task; -1: the end of the tasks, or a wait ran out
+    int kk_last;        // PV products of 16 keys in its last key tile
     uint32_t st, ph;    // K/V ring stage and its phase
     uint32_t buf;       // score buffer
     uint32_t c0, c1;    // steps of each warpgroup so far
+    uint32_t fews, fews_done;  // tasks of few rows passed, and those known to be over (fews or one less)
 
-    // Reads task `it`; false at the end of the tasks or when the wait ran out.
+    // Reads task `it`; true if it is one of the issuer's.
     template <bool kRelease>
     __device__ __forceinline__ bool open(CachedSmem &sm)
     {
+        kind = -1;
         if (!wait_task(sm, it))
             return false;
         const Task &t = sm.task[it % kTaskRing];
         const int n = t.n;
-        pair = t.pair;
+        if (n > 0)
+            kind = t.kind;
         kk_last = (t.vlast + 15) >> 4;
         if (kRelease)
             release_task(sm, it);
-        steps = pair ? 2 * n : n;
+        steps = kind == kTaskPair ? 2 * n : n;
         s = 0;
-        return n > 0;
+        return kind == kTaskSingle || kind == kTaskPair;
+    }
+
+    // Passes a task of few rows, whose key tiles the warps read themselves.
+    // The warps may start on it while they still work on the one before.
+    __device__ __forceinline__ bool pass(CachedSmem &sm)
+    {
+        pass_task(sm, it);
+        const uint32_t x = st + static_cast<uint32_t>(steps);
+        ph ^= (x / kStages) & 1u;
+        st = x % kStages;
+        ++it;
+        return fews_over(sm) && (++fews, open<true>(sm) || kind == kTaskFew);
+    }
+
+    // Waits until the warps have done with the tasks of few rows passed so
+    // far: then every ring barrier is in the phase that the cursor has it in.
+    __device__ __forceinline__ bool fews_over(CachedSmem &sm)
+    {
+        if (fews_done == fews)
+            return true;
+        if (!wait_bar(smem_u32(&sm.few_full[fews_done & 1u]), (fews_done >> 1) & 1u, &sm.ctl, kSiteFewFull))
+            return false;
+        ++fews_done;
+        return true;
     }
 
     __device__ __forceinline__ uint32_t wg() const { return static_cast<uint32_t>(s) & 1u; }
     __device__ __forceinline__ uint32_t count() const { return wg() ? c1 : c0; }
-    __device__ __forceinline__ bool last_reader() const { return !pair || wg(); }
-    __device__ __forceinline__ bool first_reader() const { return !pair || !wg(); }
+    __device__ __forceinline__ bool last_reader() const { return kind == kTaskSingle || wg(); }
+    __device__ __forceinline__ bool first_reader() const { return kind == kTaskSingle || !wg(); }
 
+    // Moves to the next step; false if the next task is not the issuer's.
     template <bool kRelease>
     __device__ __forceinline__ bool next(CachedSmem &sm)
     {
@@ -529,25 +577,35 @@ struct TaskCursor {
         buf = buf == kScoreBufs - 1 ? 0u : buf + 1;
         if (++s < steps)
             return true;
+        if (kRelease)
+            pass_task(sm, it);
         ++it;
         return open<kRelease>(sm);
     }
 };
 
+// A ring barrier that the warps release with one arrival each; the issuer
+// stands for all of them, with its last arrival when the products are done.
+__device__ __forceinline__ void commit_release(uint32_t bar)
+{
+    mbar_arrive_n(bar, kSoftmaxWarps - 1);
+    umma_commit(bar);
+}
+
 __device__ __forceinline__ void issue_score(CachedSmem &sm, uint32_t tmem, const TaskCursor &c, const TileDescs &td)
 {
     constexpr uint32_t kIdescS = idesc_bf16_f32(kBlockM, kBlockN, false);
     const uint32_t qb = static_cast<uint32_t>(c.it) & 1u;
-    const uint64_t a = td.q0 + (2 * qb + (c.pair ? c.wg() : 0u)) * kTileDescStep, b = td.k0 + c.st * kTileDescStep;
+    const uint64_t a = td.q0 + (2 * qb + (c.kind == kTaskPair ? c.wg() : 0u)) * kTileDescStep, b = td.k0 + c.st * kTileDescStep;
     const uint32_t d = tmem + c.buf * kBlockN;
 #pragma unroll
     for (int kk = 0; kk < kHeadDim / 16; ++kk)
         umma_ss(d, a + 2 * kk, b + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
     umma_commit(smem_u32(&sm.s_full[c.wg()][c.count() % 3]));
     if (c.last_reader())
-        umma_commit(smem_u32(&sm.k_empty[c.st]));
+        commit_release(smem_u32(&sm.k_empty[c.st]));
     if (c.s == c.steps - 1)
-        umma_commit(smem_u32(&sm.q_empty[qb]));
+        commit_release(smem_u32(&sm.q_empty[qb]));
 }
 
 __device__ __forceinline__ bool score_ready(CachedSmem &sm, const TaskCursor &c)
@@ -563,46 +621,58 @@ __device__ __forceinline__ void cached_mma_loop(CachedSmem &sm, uint32_t tmem)
     volatile WaitCtl *ab = &sm.ctl;
     const TileDescs td{sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024), sdesc_sw128(smem_u32(sm.k[0]), 16, 1024),
                        sdesc_sw128(smem_u32(sm.v[0]), 16, 1024)};
-    TaskCursor sc{}, vc{};  // next S, next PV to issue
-    bool s_more = sc.open<false>(sm);
-    bool v_more = vc.open<true>(sm);
-    for (int i = 0; i < kScoreBufs && s_more; ++i) {
-        if (!score_ready(sm, sc))
-            return;
-        tc_fence_after();
-        issue_score(sm, tmem, sc, td);
-        s_more = sc.next<false>(sm);
-    }
-    while (v_more) {
-        const uint32_t wg = vc.wg(), c = vc.count();
-        if (vc.first_reader() && !wait_bar(smem_u32(&sm.v_full[vc.st]), vc.ph, ab, kSiteVFull))
-            return;
-        if (!wait_bar(smem_u32(&sm.p_ready[wg][c % 3]), (c / 3) & 1u, ab, kSitePReady))
-            return;
-        tc_fence_after();
-        const uint64_t b = td.v0 + vc.st * kTileDescStep;
-        const uint32_t d = tmem + kTmemO + wg * kHeadDim, a = tmem + vc.buf * kBlockN;
-        const bool last = vc.pair ? vc.s >= vc.steps - 2 : vc.s == vc.steps - 1;  // the task's last key tile
-        const int kks = last ? vc.kk_last : kBlockN / 16;
-#pragma unroll
-        for (int kk = 0; kk < kBlockN / 16; ++kk)
-            if (kk < kks)
-                umma_ts(d, a + 8 * kk, b + 128 * kk, kIdescPV, (vc.s >= 2 || kk > 0) ? 1u : 0u);
-        umma_commit(smem_u32(&sm.o_done[wg]));
-        if (vc.s >= vc.steps - 2)  // the warpgroup's last step of the task
-            umma_commit(smem_u32(&sm.o_final[wg]));
-        if (vc.last_reader())
-            umma_commit(smem_u32(&sm.v_empty[vc.st]));
-        v_more = vc.next<true>(sm);
-        if (s_more) {
-            // S(k + 3) overwrites the buffer PV(k) reads P from.
-            if (!score_ready(sm, sc))
+    TaskCursor vc{};  // next PV to issue
+    vc.open<true>(sm);
+    for (;;) {
+        while (vc.kind == kTaskFew)
+            if (!vc.pass(sm))
                 return;
-            if (!wait_bar(smem_u32(&sm.o_done[wg]), c & 1u, ab, kSiteODone))
+        if (vc.kind < 0 || !vc.fews_over(sm))
+            return;
+        // A run of tasks for the tensor cores: the next S is up to three
+        // steps ahead, but never past a task of few rows.  (Looking further
+        // would mean waiting for tasks behind a ring full of those.)
+        TaskCursor sc = vc;  // next S to issue
+        bool s_more = true, v_more = true;
+        for (int i = 0; i < kScoreBufs && s_more; ++i) {
+            if (!score_ready(sm, sc))
                 return;
             tc_fence_after();
             issue_score(sm, tmem, sc, td);
             s_more = sc.next<false>(sm);
+        }
+        while (v_more) {
+            const uint32_t wg = vc.wg(), c = vc.count();
+            if (vc.first_reader() && !wait_bar(smem_u32(&sm.v_full[vc.st]), vc.ph, ab, kSiteVFull))
+                return;
+            if (!wait_bar(smem_u32(&sm.p_ready[wg][c % 3]), (c / 3) & 1u, ab, kSitePReady))
+                return;
+            tc_fence_after();
+            const uint64_t b = td.v0 + vc.st * kTileDescStep;
+            const uint32_t d = tmem + kTmemO + wg * kHeadDim, a = tmem + vc.buf * kBlockN;
+            const bool last = vc.kind == kTaskPair ? vc.s >= vc.steps - 2 : vc.s == vc.steps - 1;  // the last key tile
+            const int kks = last ? vc.kk_last : kBlockN / 16;
+#pragma unroll
+            for (int kk = 0; kk < kBlockN / 16; ++kk)
+                if (kk < kks)
+                    umma_ts(d, a + 8 * kk, b + 128 * kk, kIdescPV, (vc.s >= 2 || kk > 0) ? 1u : 0u);
+            umma_commit(smem_u32(&sm.o_done[wg]));
+            if (vc.s >= vc.steps - 2)  // the warpgroup's last step of the task
+                umma_commit(smem_u32(&sm.o_final[wg]));
+            if (vc.last_reader())
+                commit_release(smem_u32(&sm.v_empty[vc.st]));
+            v_more = vc.next<true>(sm);
+            if (s_more && !score_ready(sm, sc))
+                return;
+            // S(k + 3) overwrites the buffer PV(k) reads P from.  Waited for
+            // behind the run's last S too: the next run starts on free buffers.
+            if (!wait_bar(smem_u32(&sm.o_done[wg]), c & 1u, ab, kSiteODone))
+                return;
+            if (s_more) {
+                tc_fence_after();
+                issue_score(sm, tmem, sc, td);
+                s_more = sc.next<false>(sm);
+            }
         }
     }
 }
@@ -671,6 +741,214 @@ __device__ __forceinline__ void finish_cached_row(const CachedParams &p, uint32_
         p.lse[id] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
 }
 
+// A task of at most 16 rows (a single token of grouped heads, the last tokens
+// of a chunk) needs 1/8 of a 128-row tile's arithmetic and is bound by the
+// bytes of K and V, so it does without TMEM: warp w takes keys 16 w .. 16 w +
+// 15 of every key tile with 16 x 8 x 16 products on registers, keeps its own
+// softmax state and follows the K/V ring by itself; the eight states meet once,
+// at the end of the task, in the Q buffer.  Fragment layouts are those of
+// ldmatrix and mma.m16n8k16: row g = lane / 4 (and g + 8), columns 2 (lane % 4)
+// and the next.
+__device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, const Task &w, uint32_t it, uint32_t ring,
+                                     uint32_t fews, int warp)
+{
+    volatile WaitCtl *ab = &sm.ctl;
+    const int lane = threadIdx.x & 31, g = lane >> 2, c2 = 2 * (lane & 3);
+    const uint32_t qb = it & 1u;
+    uint8_t *qbuf = sm.q[qb][0];
+    const float sl2 = p.scale_log2;
+    const int rows = (w.row_end - w.row0) * p.group;
+    int lim[2];  // keys that rows g, g + 8 see, counted from this warp's first key
+    int low = 0x7fffffff;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = g + 8 * e;
+        lim[e] = 0;
+        if (r < rows) {
+            lim[e] = key_limit(w.kv, w.pos0 + r / p.group, p.unit) - w.kt0 * kBlockN - 16 * warp;
+            low = min(low, lim[e]);
+        }
+    }
+    low = __reduce_min_sync(0xffffffffu, low);
+    const int all = w.kv - w.kt0 * kBlockN - 16 * warp;  // keys that exist, counted in the same way
+
+    if (!wait_bar_warp(smem_u32(&sm.task_passed[it % (2 * kTaskRing)]), (it / (2 * kTaskRing)) & 1u, ab,
+                       kSiteTaskPassed) ||
+        !wait_bar_warp(smem_u32(&sm.q_full[qb]), (it >> 1) & 1u, ab, kSiteQFull))
+        return false;
+    uint32_t q[4][4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+        const int r = lane & 15;
+        ldmatrix_x4(smem_u32(qbuf) + r * 128 + (((2 * kk + (lane >> 4)) ^ (r & 7)) << 4), q[kk]);
+    }
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(smem_u32(&sm.few_q));
+
+    float o[8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[i][e] = 0.f;
+    // Byte offsets within a tile; the swizzle XORs a 16-byte column with the row's low 3 bits.
+    const int k_row = 16 * warp + (lane & 7), v_row = 16 * warp + (lane & 15);
+    const uint32_t k_off = k_row * 128, v_off = v_row * 128;
+    for (int j = 0; j < w.n; ++j) {
+        const uint32_t u = ring + static_cast<uint32_t>(j), st = u % kStages, ph = (u / kStages) & 1u;
+        const int here = all - j * kBlockN;  // keys of this warp's 16 that exist
+        if (!wait_bar_warp(smem_u32(&sm.k_full[st]), ph, ab, kSiteKFull))
+            return false;
+        float s[2][4] = {};
+        if (here > 0) {
+            uint32_t k[4][4];  // [key half][d half]: two 16-channel steps of B
+            const uint32_t base = smem_u32(sm.k[st]) + k_off;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                ldmatrix_x4(base + (i >> 1) * 1024 + (((4 * (i & 1) + (lane >> 3)) ^ (lane & 7)) << 4), k[i]);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    mma_16816(s[i], q[kk], k[2 * i + (kk >> 1)][2 * (kk & 1)], k[2 * i + (kk >> 1)][2 * (kk & 1) + 1]);
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_u32(&sm.k_empty[st]));
+        if (here > 0) {
+            if (low < (j + 1) * kBlockN) {  // some row may not see all of the 16 keys
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (8 * i + c2 + (e & 1) >= lim[e >> 1] - j * kBlockN)
+                            s[i][e] = -INFINITY;
+            }
+            float top[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                top[e] = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1])) * sl2;
+            // The offset moves when a logit passes it by kRescaleThreshold
+            // (P <= 2^8), so most tiles need no maximum over the lanes.
+            if (__any_sync(0xffffffffu, top[0] > m[0] + kRescaleThreshold || top[1] > m[1] + kRescaleThreshold)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 1));
+                    top[e] = fmaxf(fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], 2)), m[e]);
+                    const float f = m[e] == -INFINITY ? 0.f : ex2_approx(m[e] - top[e]);
+                    m[e] = top[e];
+                    l[e] *= f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        o[i][2 * e] *= f;
+                        o[i][2 * e + 1] *= f;
+                    }
+                }
+            }
+            uint32_t pk[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float base = m[e] == -INFINITY ? 0.f : m[e];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float a = ex2_approx(fmaf(s[i][2 * e], sl2, -base));
+                    const float b = ex2_approx(fmaf(s[i][2 * e + 1], sl2, -base));
+                    l[e] += a + b;
+                    pk[2 * i + e] = pack_bf16x2(a, b);
+                }
+            }
+            if (!wait_bar_warp(smem_u32(&sm.v_full[st]), ph, ab, kSiteVFull))
+                return false;
+            const uint32_t base = smem_u32(sm.v[st]) + v_off;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t v[4];
+                ldmatrix_x4_trans(base + (((2 * i + (lane >> 4)) ^ (lane & 7)) << 4), v);
+                if (here < 16) {
+                    // whatever lies behind the last key must not meet P = 0
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = 8 * (e & 1) + c2;
+                        v[e] &= (key < here ? 0x0000ffffu : 0u) | (key + 1 < here ? 0xffff0000u : 0u);
+                    }
+                }
+                mma_16816(o[2 * i], pk, v[0], v[1]);
+                mma_16816(o[2 * i + 1], pk, v[2], v[3]);
+            }
+        } else if (!wait_bar_warp(smem_u32(&sm.v_full[st]), ph, ab, kSiteVFull)) {
+            return false;
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(smem_u32(&sm.v_empty[st]));
+    }
+
+    // The states of the eight warps, over Q once every warp has read it:
+    // [warp][row][64] floats, pairs of columns XORed with the row against bank conflicts.
+    if (!wait_bar_warp(smem_u32(&sm.few_q), fews & 1u, ab, kSiteFewQ))
+        return false;
+    float2 *mine = reinterpret_cast<float2 *>(qbuf) + warp * (kFewRows * 32);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+        const int r = g + 8 * e;
+        if ((lane & 3) == 0)
+            sm.merge_ml[warp * kFewRows + r] = make_float2(m[e], l[e]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            mine[r * 32 + ((4 * i + (lane & 3)) ^ (g << 2))] = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+    }
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(smem_u32(&sm.few_full[fews & 1u]));
+    if (!wait_bar_warp(smem_u32(&sm.few_full[fews & 1u]), (fews >> 1) & 1u, ab, kSiteFewFull))
+        return false;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = 2 * warp + e;
+        if (r >= rows)
+            break;
+        float top = -INFINITY, sum = 0.f, a = 0.f, b = 0.f;
+        float2 ml[kSoftmaxWarps];
+#pragma unroll
+        for (int x = 0; x < kSoftmaxWarps; ++x) {
+            ml[x] = sm.merge_ml[x * kFewRows + r];
+            top = fmaxf(top, ml[x].x);
+        }
+#pragma unroll
+        for (int x = 0; x < kSoftmaxWarps; ++x) {
+            const float f = ml[x].x == -INFINITY ? 0.f : ex2_approx(ml[x].x - top);
+            const float2 v = reinterpret_cast<const float2 *>(qbuf)[(x * kFewRows + r) * 32 + (lane ^ ((r & 7) << 2))];
+            sum = fmaf(f, ml[x].y, sum);
+            a = fmaf(f, v.x, a);
+            b = fmaf(f, v.y, b);
+        }
+        const int tok = r / p.group;
+        const int64_t id = static_cast<int64_t>(w.row0 + tok) * p.H + w.hk * p.group + r - tok * p.group;
+        if (!VGGT_IN_RANGE(w.row0 + tok < p.n_rows && w.chunk < p.max_splits, kCheckAttnRow))
+            continue;
+        if (w.split) {
+            const int64_t part = static_cast<int64_t>(w.chunk) * p.n_rows * p.H + id;
+            reinterpret_cast<float2 *>(p.part_o)[part * 32 + lane] = make_float2(a, b);
+            if (lane == 0)
+                p.part_ml[part] = make_float2(top, sum);
+        } else {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            reinterpret_cast<uint32_t *>(p.o + id * kHeadDim)[lane] = pack_bf16x2(a * inv, b * inv);
+            if (p.lse && lane == 0)
+                p.lse[id] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+        }
+    }
+    // This warp's reads and writes come before the next Q tile is copied over them.
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(smem_u32(&sm.q_empty[qb]));
+    return true;
+}
+
 __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem, const CachedParams &p, int wg)
 {
     volatile WaitCtl *ab = &sm.ctl;
@@ -691,6 +969,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
     uint32_t ring = 0;       // key tiles before the task
     uint32_t c = 0;          // steps of this warpgroup
     uint32_t finals = 0;     // tasks in which it had a step
+    uint32_t fews = 0;       // tasks of few rows so far
     uint32_t merges = 0;     // single-tile tasks that both warpgroups worked on
     bool merge_open = false; // warpgroup 1: its last merge has not been read yet
 
@@ -705,11 +984,18 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
             release_task(sm, it);
         if (w.n == 0)
             return;
-        const int tile_tok = (w.pair && wg ? p.tile_tokens : 0) + tok;  // token within the task
+        if (w.kind == kTaskFew) {
+            if (!run_few(sm, p, w, static_cast<uint32_t>(it), ring, fews, wg * 4 + (t >> 5)))
+                return;
+            ++fews;
+            ring += static_cast<uint32_t>(w.n);
+            continue;
+        }
+        const int tile_tok = (w.kind == kTaskPair && wg ? p.tile_tokens : 0) + tok;  // token within the task
         const int row = w.row0 + tile_tok;
         const bool row_ok = tok < p.tile_tokens && row < w.row_end;
         const int head = w.hk * p.group + tile_head;
-        const int steps = w.pair ? w.n : (w.n + 1 - wg) >> 1;  // of this warpgroup
+        const int steps = w.kind == kTaskPair ? w.n : (w.n + 1 - wg) >> 1;  // of this warpgroup
         // keys this row sees, counted from the task's first key
         const int lim = row_ok ? key_limit(w.kv, w.pos0 + tile_tok, p.unit) - w.kt0 * kBlockN : 0;
         const bool warp_ok = __any_sync(0xffffffffu, row_ok);
@@ -717,12 +1003,12 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
         float m = -INFINITY, l = 0.f;
 
         for (int x = 0; x < steps; ++x, ++c) {
-            const int j = w.pair ? x : 2 * x + wg;  // key tile within the task
+            const int j = w.kind == kTaskPair ? x : 2 * x + wg;  // key tile within the task
             const uint32_t buf = (k0 + static_cast<uint32_t>(2 * x + wg)) % kScoreBufs;
             const uint32_t tS = tmem + buf * kBlockN + lane_off;
             if (!wait_bar_warp(bar_s + 8 * (c % 3), (c / 3) & 1, ab, kSiteSFull))
                 return;
-            if (j == w.n - 1 && (w.vlast & 15) != 0 && (!w.pair || wg == 0)) {
+            if (j == w.n - 1 && (w.vlast & 15) != 0 && (w.kind != kTaskPair || wg == 0)) {
                 // V rows behind the last key, up to the end of its group of 16
                 const uint32_t u = ring + static_cast<uint32_t>(j), st = u % kStages;
                 if (!wait_bar_warp(smem_u32(&sm.v_full[st]), (u / kStages) & 1, ab, kSiteVFull))
@@ -856,7 +1142,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
             if ((threadIdx.x & 31) == 0)
                 mbar_arrive(bar_p + 8 * (c % 3));
         }
-        k0 += static_cast<uint32_t>(w.pair ? 2 * w.n : w.n);
+        k0 += static_cast<uint32_t>(w.kind == kTaskPair ? 2 * w.n : w.n);
         ring += static_cast<uint32_t>(w.n);
 
         if (steps == 0)
@@ -865,7 +1151,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
             return;
         ++finals;
         tc_fence_after();
-        const bool merged = !w.pair && w.n > 1;
+        const bool merged = w.kind == kTaskSingle && w.n > 1;
         if (merged && wg == 1) {
             if (merge_open && !wait_bar_warp(smem_u32(&sm.merge_free), (merges - 1) & 1, ab, kSiteMergeFree))
                 return;
@@ -918,7 +1204,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.q_full[i]), 1);
-            mbar_init(smem_u32(&sm.q_empty[i]), 1);
+            mbar_init(smem_u32(&sm.q_empty[i]), kSoftmaxWarps);
             for (int c = 0; c < 3; ++c) {
                 mbar_init(smem_u32(&sm.s_full[i][c]), 1);
                 mbar_init(smem_u32(&sm.p_ready[i][c]), 4);
@@ -928,9 +1214,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&sm.k_full[i]), 1);
-            mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.k_empty[i]), kSoftmaxWarps);
             mbar_init(smem_u32(&sm.v_full[i]), 1);
-            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v_empty[i]), kSoftmaxWarps);
         }
         for (int i = 0; i < kTaskRing; ++i) {
             mbar_init(smem_u32(&sm.task_full[i]), 1);
@@ -938,6 +1224,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         mbar_init(smem_u32(&sm.merge_ready), 4);
         mbar_init(smem_u32(&sm.merge_free), 4);
+        mbar_init(smem_u32(&sm.few_q), kSoftmaxWarps);
+        for (int i = 0; i < 2; ++i)
+            mbar_init(smem_u32(&sm.few_full[i]), kSoftmaxWarps);
+        for (int i = 0; i < 2 * kTaskRing; ++i)
+            mbar_init(smem_u32(&sm.task_passed[i]), 1);
         mbar_init(smem_u32(&sm.drain), 1);
         sm.ctl.abort = 0;
         sm.ctl.limit_ns = p.wait_limit_ns;

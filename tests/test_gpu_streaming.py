@@ -180,6 +180,24 @@ def test_attention_matches_64_bits(case):
     assert (got[b.cu[-1]:] == 9.0).all()  # rows behind the last sequence
 
 
+@pytest.mark.parametrize("heads,kv_heads,unit,seed", [(16, 8, 1, 1), (4, 4, 0, 2), (16, 1, 30, 3), (21, 3, 1, 4)])
+def test_attention_of_many_sequences_of_every_kind(heads, kv_heads, unit, seed):
+    """Several hundred sequences, so that every CTA works through many tasks: single tokens, a few rows, one tile,
+    an odd and an even number of tiles, rows without keys, and long runs of sequences without any."""
+    rng = np.random.default_rng(seed)
+    new, kv = [], []
+    for _ in range(260):
+        n = int(rng.choice([0, 1, 1, 1, 2, 5, 17, 60, 130, 260, 400]))
+        new.append(n)
+        kv.append(int(rng.choice([0, max(0, n - 3), n, n + int(rng.integers(0, 500)), int(rng.integers(1, 40))])))
+    new[100:100] = [2] * 2600
+    kv[100:100] = [0] * 2600
+    b = ref.Batch(kv, new, 16, heads, kv_heads, seed=seed)
+    got, lse = attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, causal_unit=unit, want_lse=True)
+    ok()
+    check_attention(b, unit, got, lse)
+
+
 @pytest.mark.parametrize("layout", ["token", "both"])
 @pytest.mark.parametrize("unit", [0, 1, 50])
 def test_attention_over_other_cache_layouts_and_strided_queries(layout, unit):
