@@ -9,26 +9,27 @@
 // tile holds F = floor(128 / G) consecutive tokens of a sequence, G rows each,
 // so a key tile is read once for all of them.
 //
-// Work.  A task is a range of 128-key tiles of one key head for
+// Work.  A unit is, for one key head of a sequence,
 //  * a pair of query tiles: both read one K/V stream, one softmax warpgroup
-//    each (two steps per key tile); or
-//  * a single query tile (the last of an odd number, every single-token
-//    sequence): the warpgroups take the key tiles in turn (one step per key
-//    tile) and warpgroup 0 merges the two softmax states at the end.
-// A step costs the same in both: 4.2 MFLOP on the tensor cores, or 32 KB of
-// K and V per step of a single tile, about 0.7 us of an SM's share of either.
-// Ranges are cut to at most `steps` steps, so one sequence and few rows fill
-// the GPU too.  Every CTA finds the same `steps` from the lengths (see
-// plan_tasks): no host copy of the lengths, no launch before this one.  Tasks
-// are numbered with the pairs of a head and key range innermost and dealt out
-// in turn, so that the CTAs that read the same keys do so at the same time.
-// The parts of a cut range leave (m, l) and the sum of P V in fp32 in the
-// workspace, and cached_combine_kernel joins them in order.
+//    each (two steps per key tile);
+//  * a single query tile (the last of an odd number): the warpgroups take the
+//    key tiles in turn (one step per key tile) and warpgroup 0 merges the two
+//    softmax states at the end; or
+//  * the same with at most 16 rows (a single token of grouped heads): the
+//    eight softmax warps multiply on registers, see run_few.
+// A step costs about the same in all: 4.2 MFLOP on the tensor cores, or the 32
+// KB of K and V of a key tile, 0.7 us of an SM's share of either.  The units
+// stand in one line (sequence, head, tile), and CTA i takes the i-th of equal
+// parts of their steps, wherever that cuts them: no CTA waits for another, no
+// host copy of the lengths is needed, and every CTA finds its part from the
+// lengths by itself.  A unit that is cut leaves (m, l) and the sum of P V of
+// its parts in fp32 in the workspace, two slots per CTA, and
+// cached_combine_kernel joins them in order.
 //
-// CTA (384 threads, one per SM): warp 0 loads Q, K and V by TMA, page by page
-// (a 4-D map of the pages; a box is the largest power of two of rows that
-// divides the page, at most 128), warp 1 issues the UMMAs, warp 2 decodes
-// tasks ahead into a ring, warps 4-7 and 8-11 are the softmax warpgroups.
+// CTA (384 threads, one per SM): warps 0 and 3 load Q and K, and V, by TMA, page
+// by page (a 4-D map of the pages; a box is the largest power of two of rows
+// that divides the page, at most 128), warp 1 issues the UMMAs, warp 2 walks
+// along the CTA's work and writes its tasks into a ring, warps 4-7 and 8-11 are the softmax warpgroups.
 // TMEM, score buffers and the order S(k+3) after PV(k) are those of
 // attn_fwd_kernel.
 //
@@ -49,12 +50,11 @@
 
 namespace vggt {
 
-constexpr int kMaxSplits = 128;
+constexpr int kMaxCtas = 148;
 constexpr int kTaskRing = 8;
-constexpr int kNoSplit = 0x7fffffff;
-// Cost of a task beside its steps (Q load, first score, epilogue) and of the
-// joining launch, in steps: used to choose `steps` only.
-constexpr float kTaskOverhead = 4.f, kJoinOverhead = 4.f;
+// What a unit costs beside its steps (Q load, first score, epilogue), in
+// steps, and the fewest steps a CTA is used for.
+constexpr int kUnitCost = 6, kFewUnitCost = 1, kMinSteps = 4;
 
 constexpr int kFewRows = 16;      // rows of a task that the warps work on by themselves
 constexpr int kSoftmaxWarps = 8;  // and with how many: 16 keys of a tile each
@@ -62,17 +62,24 @@ constexpr int kSoftmaxWarps = 8;  // and with how many: 16 keys of a tile each
 enum : uint32_t { kSiteTaskFull = 12, kSiteTaskEmpty, kSiteMergeReady, kSiteMergeFree, kSiteFewQ, kSiteFewFull, kSiteTaskPassed };
 enum : int { kTaskSingle = 0, kTaskPair = 1, kTaskFew = 2 };
 
+// What a CTA leaves for the joining launch: the unit whose first part, but not
+// its last, was its work.  Parts 1, 2, ... are those of the CTAs behind it.
+struct Join {
+    int row0, rows, hk, parts;  // parts = 0: none
+};
+
 struct CachedParams {
     int n_seqs, n_rows, H, Hkv, group, tile_tokens;  // group G = H / Hkv, tile_tokens F
     int page_size, n_pages, max_pages, unit, box_rows;
-    int max_splits;  // most parts of a row's keys; 1: no workspace
+    int cost_shift;  // costs are counted in 2^cost_shift steps, so that their sum fits in 31 bits
+    int part_rows;   // rows of a workspace slot
     float scale_log2;
     const int32_t *table, *cu_rows, *kv_lens;
     __nv_bfloat16 *o;
     float *lse;
-    int32_t *header;  // workspace: [0] = steps
-    float2 *part_ml;  // [max_splits][n_rows * H]
-    float *part_o;    // [max_splits][n_rows * H][64]
+    Join *join;       // workspace: [kMaxCtas]
+    float2 *part_ml;  // [2 * kMaxCtas][part_rows]; slot 2 i: CTA i's part that starts inside a unit, 2 i + 1: at its start
+    float *part_o;    // [2 * kMaxCtas][part_rows][64]
     unsigned long long wait_limit_ns;
 };
 
@@ -81,7 +88,7 @@ struct Task {
     int pos0, kv;       // position of row0's token, keys of the sequence
     int kt0, n;         // first key tile, key tiles (0: the end of the CTA's tasks)
     int b, hk;
-    int kind, split, chunk;
+    int kind, slot;     // slot of the workspace, -1: the whole unit
     int vlast;          // keys of the last tile that exist, 1..128
 };
 
@@ -103,10 +110,9 @@ struct __align__(1024) CachedSmem {
     uint64_t drain;
     uint32_t tmem_base;
     WaitCtl ctl;
-    int cand_tasks[kMaxSplits];
-    int longest, work, steps, n_tasks;
+    int work;
     int scan[kAttnThreads / 32];
-    int task_end[1];  // [n_seqs]: tasks up to and with the sequence
+    int work_end[1];  // [n_seqs]: cost of the units up to and with the sequence
 };
 
 constexpr size_t cached_smem_bytes(int n_seqs)
@@ -152,194 +158,98 @@ __device__ __forceinline__ int pair_tiles(const CachedParams &p, const Seq &s, i
     return key_tiles(p, s, min(s.n, (2 * pr + 2) * p.tile_tokens) - 1);
 }
 
-__device__ __forceinline__ int parts_of(int tiles, int most)
+// The units of one key head of a sequence: pairs first, then the single tile.
+__device__ __forceinline__ int unit_count(const CachedParams &p, const Seq &s)
 {
-    return tiles <= most ? 1 : (tiles - 1) / most + 1;
+    return ((s.n + p.tile_tokens - 1) / p.tile_tokens + 1) >> 1;
 }
 
-__device__ __forceinline__ int pair_step_tiles(int steps)
-{
-    return (steps >> 1) + (steps & 1);
-}
-
-// Tasks of one key head of a sequence: pairs first, then the single tile.
-struct SeqTasks {
-    int pairs, single;
+struct Unit {
+    int kind, tiles, cost;
 };
 
-__device__ __forceinline__ SeqTasks seq_tasks(const CachedParams &p, const Seq &s, int steps)
+__device__ __forceinline__ Unit unit_of(const CachedParams &p, const Seq &s, int i)
 {
-    SeqTasks t{0, 0};
-    if (s.n == 0)
-        return t;
-    const int tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens, pairs = tiles >> 1, c = pair_step_tiles(steps);
-    if (pairs > 0) {
-        const int lo = parts_of(pair_tiles(p, s, 0), c), hi = parts_of(pair_tiles(p, s, pairs - 1), c);
-        if (lo == hi) {
-            t.pairs = pairs * lo;
-        } else {
-            for (int i = 0; i < pairs; ++i)
-                t.pairs += parts_of(pair_tiles(p, s, i), c);
-        }
-    }
-    if (tiles & 1)
-        t.single = parts_of(key_tiles(p, s, s.n - 1), steps);
-    return t;
+    Unit u;
+    const int left = s.n - 2 * i * p.tile_tokens;
+    u.kind = left > p.tile_tokens ? kTaskPair : (left * p.group <= kFewRows ? kTaskFew : kTaskSingle);
+    u.tiles = pair_tiles(p, s, i);
+    const int steps = (u.kind == kTaskPair ? 2 * u.tiles : u.tiles) + (u.kind == kTaskFew ? kFewUnitCost : kUnitCost);
+    u.cost = u.tiles == 0 ? 1 : ((steps - 1) >> p.cost_shift) + 1;
+    return u;
 }
 
-// Chooses the largest number of steps of a task and counts the tasks; every
-// CTA of the launch comes to the same.  A candidate cuts the longest range
-// into s parts; its time is taken as the rounds of the CTAs over tasks of
-// that many steps, or, where the tasks are uneven, as the evenly shared work
-// and one task more, whichever is less.
-__device__ __forceinline__ void plan_tasks(CachedSmem &sm, const CachedParams &p)
+// Key tiles of a unit before point x of its cost.
+__device__ __forceinline__ int tiles_before(const CachedParams &p, const Unit &u, int x)
 {
-    const int tid = threadIdx.x, cap = p.max_splits;
-    if (tid < kMaxSplits)
-        sm.cand_tasks[tid] = 0;
-    if (tid == 0) {
-        sm.longest = 1;
-        sm.work = 0;
-        sm.steps = kNoSplit;
-    }
-    __syncthreads();
-    if (cap > 1) {
-        int longest = 0, work = 0;
-        for (int b = tid; b < p.n_seqs; b += kAttnThreads) {
-            const Seq s = load_seq(p, b);
-            if (s.n == 0)
-                continue;
-            const int tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens, pairs = tiles >> 1;
-            const int kt = key_tiles(p, s, s.n - 1);
-            longest = max(longest, pairs ? 2 * kt : kt);
-            work += tiles * kt;
-        }
-        atomicMax(&sm.longest, longest);
-        atomicAdd(&sm.work, work);
-        __syncthreads();
-        const int total = cap * p.n_seqs;
-        longest = sm.longest;
-        for (int i = tid; i < total; i += kAttnThreads) {
-            const int b = i / cap, c = i - b * cap;
-            const SeqTasks t = seq_tasks(p, load_seq(p, b), (longest + c) / (c + 1));
-            atomicAdd(&sm.cand_tasks[c], t.pairs + t.single);
-        }
-        __syncthreads();
-        if (tid < 32) {
-            const float grid = static_cast<float>(gridDim.x);
-            float best = INFINITY;
-            int at = 0;
-            for (int c = tid; c < cap; c += 32) {
-                const float n = static_cast<float>(sm.cand_tasks[c]) * p.Hkv;
-                const float each = static_cast<float>((longest + c) / (c + 1)) + kTaskOverhead;
-                const float even = (static_cast<float>(sm.work) * p.Hkv + n * kTaskOverhead) / grid + each;
-                const float t = fminf(ceilf(n / grid) * each, even) + (c > 0 ? kJoinOverhead : 0.f);
-                if (t < best) {
-                    best = t;
-                    at = c;
-                }
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) {
-                const float t = __shfl_xor_sync(0xffffffffu, best, d);
-                const int a = __shfl_xor_sync(0xffffffffu, at, d);
-                if (t < best || (t == best && a < at)) {
-                    best = t;
-                    at = a;
-                }
-            }
-            if (tid == 0) {
-                sm.steps = at > 0 ? (longest + at) / (at + 1) : kNoSplit;
-                if (blockIdx.x == 0)
-                    p.header[0] = sm.steps;
-            }
-        }
-        __syncthreads();
-    }
-    // Tasks up to and with every sequence: runs of consecutive sequences per thread.
-    const int steps = sm.steps;
+    int steps = (x << p.cost_shift) - (u.kind == kTaskFew ? kFewUnitCost : kUnitCost);
+    if (u.kind == kTaskPair)
+        steps >>= 1;
+    return max(0, min(steps, u.tiles));
+}
+
+// Sums the costs: work_end and work.  Every thread takes a run of consecutive
+// sequences; one with many pairs of unequal length is summed by its warp.
+__device__ __forceinline__ void plan_work(CachedSmem &sm, const CachedParams &p)
+{
+    constexpr int kLong = 8;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int per = (p.n_seqs + kAttnThreads - 1) / kAttnThreads;
-    const int b0 = min(tid * per, p.n_seqs), b1 = min(b0 + per, p.n_seqs);
     int mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const SeqTasks t = seq_tasks(p, load_seq(p, b), steps);
-        mine += (t.pairs + t.single) * p.Hkv;
-        sm.task_end[b] = mine;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        Seq s{0, 0, 0};
+        if (b < p.n_seqs)
+            s = load_seq(p, b);
+        const int units = unit_count(p, s);
+        int sum = 0;
+        bool loop = false;
+        if (units > 0) {
+            const Unit last = unit_of(p, s, units - 1);
+            sum = last.cost;
+            if (units > 1) {
+                const Unit first = unit_of(p, s, 0), other = unit_of(p, s, units - 2);
+                if (first.cost == other.cost)
+                    sum += (units - 1) * first.cost;
+                else if (units <= kLong)
+                    for (int j = 0; j < units - 1; ++j)
+                        sum += unit_of(p, s, j).cost;
+                else
+                    loop = true;
+            }
+        }
+        for (unsigned todo = __ballot_sync(0xffffffffu, loop); todo; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1;
+            const Seq x{__shfl_sync(0xffffffffu, s.row0, src), __shfl_sync(0xffffffffu, s.n, src),
+                        __shfl_sync(0xffffffffu, s.kv, src)};
+            int part = 0;
+            for (int j = lane; j < unit_count(p, x) - 1; j += 32)
+                part += unit_of(p, x, j).cost;
+            part = __reduce_add_sync(0xffffffffu, part);
+            if (lane == src)
+                sum += part;
+        }
+        mine += sum * p.Hkv;
+        if (b < p.n_seqs)
+            sm.work_end[b] = mine;
     }
     int upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, upto, d);
-        if ((tid & 31) >= d)
+        if (lane >= d)
             upto += x;
     }
-    if ((tid & 31) == 31)
+    if (lane == 31)
         sm.scan[tid >> 5] = upto;
     __syncthreads();
     for (int w = 0; w < (tid >> 5); ++w)
         upto += sm.scan[w];
-    for (int b = b0; b < b1; ++b)
-        sm.task_end[b] += upto - mine;
+    if (upto != mine)
+        for (int b = tid * per; b < min((tid + 1) * per, p.n_seqs); ++b)
+            sm.work_end[b] += upto - mine;
     if (tid == kAttnThreads - 1)
-        sm.n_tasks = upto;
-    __syncthreads();
-}
-
-__device__ __forceinline__ Task decode_task(const CachedSmem &sm, const CachedParams &p, int i)
-{
-    const int steps = sm.steps, b = upper_bound(sm.task_end, p.n_seqs, i);
-    const int first = b ? sm.task_end[b - 1] : 0, per_head = (sm.task_end[b] - first) / p.Hkv;
-    const Seq s = load_seq(p, b);
-    const int tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens, pairs = tiles >> 1;
-    const int tiles_all = key_tiles(p, s, s.n - 1);
-    const int single = (tiles & 1) ? parts_of(tiles_all, steps) : 0;
-    Task t;
-    t.b = b;
-    t.hk = (i - first) / per_head;
-    int r = i - first - t.hk * per_head, total, most;
-    if (r < per_head - single) {
-        t.kind = kTaskPair;
-        most = pair_step_tiles(steps);
-        // The first parts hold every pair; the later ones those whose limit reaches them.
-        const int whole = parts_of(pair_tiles(p, s, 0), most);
-        int pr;
-        if (r < whole * pairs) {
-            t.chunk = r / pairs;
-            pr = r - t.chunk * pairs;
-        } else {
-            r -= whole * pairs;
-            for (t.chunk = whole;; ++t.chunk) {
-                int lo = 0, hi = pairs - 1;  // the last pair reaches every part
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (pair_tiles(p, s, mid) > t.chunk * most)
-                        hi = mid;
-                    else
-                        lo = mid + 1;
-                }
-                pr = lo + r;
-                if (pr < pairs)
-                    break;
-                r -= pairs - lo;
-            }
-        }
-        total = pair_tiles(p, s, pr);
-        t.row0 = s.row0 + 2 * pr * p.tile_tokens;
-    } else {
-        t.kind = (s.n - 2 * pairs * p.tile_tokens) * p.group <= kFewRows ? kTaskFew : kTaskSingle;
-        most = steps;
-        t.chunk = r - (per_head - single);
-        total = tiles_all;
-        t.row0 = s.row0 + 2 * pairs * p.tile_tokens;
-    }
-    t.split = total > most;
-    t.kt0 = t.split ? t.chunk * most : 0;
-    t.n = min(total - t.kt0, most);
-    t.row_end = s.row0 + s.n;
-    t.pos0 = s.kv - (t.row_end - t.row0);
-    t.kv = s.kv;
-    t.vlast = min(kBlockN, s.kv - (t.kt0 + t.n - 1) * kBlockN);
-    return t;
+        sm.work = upto;
 }
 
 // --------------------------------------------------------------- roles
@@ -358,38 +268,102 @@ __device__ __forceinline__ void write_empty_rows(const CachedParams &p, int row0
     }
 }
 
-// Warp 2: the lanes decode 32 tasks at once and hand on, in order, those with
-// keys, then one with n = 0 that ends the list.  Tasks without keys (their
-// sequence was refused pages, e.g.) are dealt with here and never enter the
-// ring: the issuer looks ahead to the next task with keys while it still has
-// products of earlier ones to issue, so it must not have to pass a ring full
-// of empty ones.
-__device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &p, int my_tasks)
+// Warp 2: walks along the CTA's part of the work and hands on its tasks, then
+// one with n = 0 that ends the list.  Units without keys (their sequence was
+// refused pages, e.g.) are dealt with here and never enter the ring.
+__device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &p)
 {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, cta = static_cast<int>(blockIdx.x);
+    const int64_t work = sm.work;
+    const int64_t ctas = max(int64_t{1}, min(static_cast<int64_t>(gridDim.x), (work << p.cost_shift) / kMinSteps));
+    Join join{0, 0, 0, 0};
+    int w = 0, w1 = 0;
+    if (cta < ctas) {
+        w = static_cast<int>(cta * work / ctas);
+        w1 = static_cast<int>((cta + 1) * work / ctas);
+    }
     uint32_t it = 0;
-    for (int base = 0; base <= my_tasks; base += 32) {
-        Task t{};
-        if (base + lane < my_tasks)
-            t = decode_task(sm, p, static_cast<int>(blockIdx.x + (base + lane) * gridDim.x));
-        const int m = min(32, my_tasks + 1 - base);
-        for (int i = 0; i < m; ++i) {
-            if (base + i < my_tasks && __shfl_sync(0xffffffffu, t.n, i) == 0) {
-                write_empty_rows(p, __shfl_sync(0xffffffffu, t.row0, i), __shfl_sync(0xffffffffu, t.row_end, i),
-                                 __shfl_sync(0xffffffffu, t.kind, i), __shfl_sync(0xffffffffu, t.hk, i));
-                continue;
+    auto push = [&](const Task &t) -> bool {
+        const uint32_t slot = it % kTaskRing;
+        if (!wait_bar_warp(smem_u32(&sm.task_empty[slot]), ((it / kTaskRing) & 1) ^ 1, &sm.ctl, kSiteTaskEmpty))
+            return false;
+        if (lane == 0) {
+            sm.task[slot] = t;
+            mbar_arrive(smem_u32(&sm.task_full[slot]));
+        }
+        __syncwarp();
+        ++it;
+        return true;
+    };
+    while (w < w1) {
+        // The sequence, head and unit at point w, and x, its place in the unit.
+        const int b = upper_bound(sm.work_end, p.n_seqs, w);
+        const int first = b ? sm.work_end[b - 1] : 0, per_head = (sm.work_end[b] - first) / p.Hkv;
+        const Seq s = load_seq(p, b);
+        const int units = unit_count(p, s);
+        int hk = (w - first) / per_head, x = w - first - hk * per_head, i = 0;
+        for (;; i += 32) {
+            const int cost = i + lane < units ? unit_of(p, s, i + lane).cost : 0;
+            int upto = cost;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d)
+                    upto += y;
             }
-            const uint32_t slot = it % kTaskRing;
-            if (!wait_bar_warp(smem_u32(&sm.task_empty[slot]), ((it / kTaskRing) & 1) ^ 1, &sm.ctl, kSiteTaskEmpty))
-                return;
-            if (lane == i) {
-                sm.task[slot] = t;
-                mbar_arrive(smem_u32(&sm.task_full[slot]));
+            const unsigned over = __ballot_sync(0xffffffffu, upto > x);
+            if (over || i + 32 >= units) {
+                const int at = over ? __ffs(over) - 1 : 31;
+                x -= __shfl_sync(0xffffffffu, upto - cost, at);
+                i += at;
+                break;
             }
-            __syncwarp();
-            ++it;
+            x -= __shfl_sync(0xffffffffu, upto, 31);
+        }
+        while (w < w1 && hk < p.Hkv) {
+            const Unit u = unit_of(p, s, i);
+            const int x1 = min(u.cost, x + w1 - w);
+            Task t;
+            t.row0 = s.row0 + 2 * i * p.tile_tokens;
+            t.row_end = s.row0 + s.n;
+            t.hk = hk;
+            t.kind = u.kind;
+            if (u.tiles == 0) {
+                if (x == 0)
+                    write_empty_rows(p, t.row0, t.row_end, t.kind, t.hk);
+            } else {
+                t.kt0 = tiles_before(p, u, x);
+                t.n = tiles_before(p, u, x1) - t.kt0;
+                t.b = b;
+                t.pos0 = s.kv - (t.row_end - t.row0);
+                t.kv = s.kv;
+                t.vlast = min(kBlockN, s.kv - (t.kt0 + t.n - 1) * kBlockN);
+                t.slot = -1;
+                if (t.n > 0 && t.n < u.tiles) {
+                    t.slot = 2 * cta + (t.kt0 == 0);
+                    if (t.kt0 == 0) {
+                        // up to the CTA that has the unit's last point
+                        const int64_t end = static_cast<int64_t>(w) - x + u.cost;
+                        join.row0 = t.row0;
+                        join.rows = min(t.row_end - t.row0, 2 * p.tile_tokens) * p.group;
+                        join.hk = hk;
+                        join.parts = static_cast<int>((end * ctas + work - 1) / work) - cta;
+                    }
+                }
+                if (t.n > 0 && !push(t))
+                    return;
+            }
+            w += x1 - x;
+            x = 0;
+            if (++i == units) {
+                i = 0;
+                ++hk;
+            }
         }
     }
+    if (lane == 0)
+        p.join[cta] = join;
+    push(Task{});
 }
 
 // Reads task `it` from the ring (the caller releases it once read).
@@ -404,15 +378,22 @@ __device__ __forceinline__ void release_task(CachedSmem &sm, int it)
     mbar_arrive(smem_u32(&sm.task_empty[it % kTaskRing]));
 }
 
-__device__ __forceinline__ void run_cached_producer(CachedSmem &sm, const CUtensorMap *tmQ, const CUtensorMap *tmK,
-                                                    const CUtensorMap *tmV, const CachedParams &p)
+// Warp 0 loads Q and K, warp 3 V: the copies of a tile of small pages are many
+// (16 of 2 KB for pages of 16), and a warp issues those of its lanes one after
+// another.
+template <bool kIsV>
+__device__ __forceinline__ void run_cached_producer(CachedSmem &sm, const CUtensorMap *tmQ, const CUtensorMap *tmKV,
+                                                    const CachedParams &p)
 {
     volatile WaitCtl *ab = &sm.ctl;
     const int lane = threadIdx.x & 31;
     const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * kHeadDim * 2;
     const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * kHeadDim * 2;
-    uint32_t u = 0, k_issued = 0, v_issued = 0, qn = 0;
-    for (int it = 0;; ++it) {
+    const uint32_t full = smem_u32(kIsV ? sm.v_full : sm.k_full), empty = smem_u32(kIsV ? sm.v_empty : sm.k_empty);
+    const uint32_t tiles = smem_u32(kIsV ? sm.v[0] : sm.k[0]);
+    uint32_t issued = 0;
+    int it = 0;
+    for (;; ++it) {
         const bool got = wait_task(sm, it);
         __syncwarp();
         if (!__all_sync(0xffffffffu, got))
@@ -439,53 +420,47 @@ __device__ __forceinline__ void run_cached_producer(CachedSmem &sm, const CUtens
                 return p.n_pages;  // outside the map: the box is filled with zeros
             };
             int page = lookup(0);
-            const int qb = static_cast<int>(qn & 1);
-            if (!wait_bar_warp(smem_u32(&sm.q_empty[qb]), ((qn >> 1) & 1) ^ 1, ab, kSiteQEmpty))
-                goto out;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(smem_u32(&sm.q_full[qb]), pair ? 2 * q_bytes : q_bytes);
-                tma_load_3d(smem_u32(sm.q[qb][0]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group, row0);
-                if (pair)
-                    tma_load_3d(smem_u32(sm.q[qb][1]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group,
-                                row0 + p.tile_tokens);
+            if (!kIsV) {
+                const int qb = it & 1;
+                if (!wait_bar_warp(smem_u32(&sm.q_empty[qb]), ((static_cast<uint32_t>(it) >> 1) & 1) ^ 1, ab, kSiteQEmpty))
+                    goto out;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(smem_u32(&sm.q_full[qb]), pair ? 2 * q_bytes : q_bytes);
+                    tma_load_3d(smem_u32(sm.q[qb][0]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group, row0);
+                    if (pair)
+                        tma_load_3d(smem_u32(sm.q[qb][1]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group,
+                                    row0 + p.tile_tokens);
+                }
             }
-            ++qn;
-            for (int j = 0; j < n; ++j, ++u) {
+            for (int j = 0; j < n; ++j) {
                 const int valid = j == n - 1 ? vlast : kBlockN;
                 const int boxes = (valid + p.box_rows - 1) / p.box_rows;
                 const int off = ((kt0 + j) * kBlockN + lane * p.box_rows) % p.page_size;
                 const int here = page;
                 if (j + 1 < n)
                     page = lookup(j + 1);
-                const uint32_t st = u % kStages, ph = ((u / kStages) & 1) ^ 1;
-                if (!wait_bar_warp(smem_u32(&sm.k_empty[st]), ph, ab, kSiteKEmpty))
+                const uint32_t st = issued % kStages;
+                if (!wait_bar_warp(empty + 8 * st, ((issued / kStages) & 1) ^ 1, ab, kIsV ? kSiteVEmpty : kSiteKEmpty)) {
+                    ++it;
                     goto out;
+                }
                 if (lane == 0)
-                    mbar_arrive_expect_tx(smem_u32(&sm.k_full[st]), boxes * box_bytes);
-                ++k_issued;
+                    mbar_arrive_expect_tx(full + 8 * st, boxes * box_bytes);
+                ++issued;
                 __syncwarp();
                 if (lane < boxes)
-                    tma_load_4d(smem_u32(sm.k[st]) + lane * box_bytes, tmK, smem_u32(&sm.k_full[st]), 0, off, hk, here);
-                if (!wait_bar_warp(smem_u32(&sm.v_empty[st]), ph, ab, kSiteVEmpty))
-                    goto out;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(smem_u32(&sm.v_full[st]), boxes * box_bytes);
-                ++v_issued;
-                __syncwarp();
-                if (lane < boxes)
-                    tma_load_4d(smem_u32(sm.v[st]) + lane * box_bytes, tmV, smem_u32(&sm.v_full[st]), 0, off, hk, here);
+                    tma_load_4d(tiles + st * kTileBytes + lane * box_bytes, tmKV, full + 8 * st, 0, off, hk, here);
             }
         }
     }
 out:
-    // Every copy this warp started must land before the CTA may exit.
+    // Every copy this warp started must land before the CTA may exit; `it` is
+    // the number of Q tiles.
     __syncwarp();
     if (lane == 0) {
-        for (uint32_t i = (k_issued > kStages ? k_issued - kStages : 0); i < k_issued; ++i)
-            wait_drain(smem_u32(&sm.k_full[i % kStages]), (i / kStages) & 1);
-        for (uint32_t i = (v_issued > kStages ? v_issued - kStages : 0); i < v_issued; ++i)
-            wait_drain(smem_u32(&sm.v_full[i % kStages]), (i / kStages) & 1);
-        for (uint32_t i = (qn > 2 ? qn - 2 : 0); i < qn; ++i)
+        for (uint32_t i = (issued > kStages ? issued - kStages : 0); i < issued; ++i)
+            wait_drain(full + 8 * (i % kStages), (i / kStages) & 1);
+        for (int i = (it > 2 ? it - 2 : 0); !kIsV && i < it; ++i)
             wait_drain(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1);
     }
     __syncwarp();
@@ -695,9 +670,11 @@ __device__ __forceinline__ void finish_cached_row(const CachedParams &p, uint32_
                                                   float l, float m)
 {
     const int64_t id = static_cast<int64_t>(row) * p.H + h;
-    const bool go = row_ok && VGGT_IN_RANGE(row >= 0 && row < p.n_rows && h < p.H && t.chunk < p.max_splits,
+    const int64_t part = static_cast<int64_t>(t.slot) * p.part_rows + (row - t.row0) * p.group + h - t.hk * p.group;
+    const bool go = row_ok && VGGT_IN_RANGE(row >= 0 && row < p.n_rows && h < p.H &&
+                                                (row - t.row0 + 1) * p.group <= (t.slot < 0 ? 256 : p.part_rows),
                                             kCheckAttnRow);
-    const float f = t.split ? 1.f : (l == 0.f ? 0.f : 1.f / l);
+    const float f = t.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
     const float f0 = merged ? w0 * f : f, f1 = w1 * f;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
@@ -719,9 +696,8 @@ __device__ __forceinline__ void finish_cached_row(const CachedParams &p, uint32_
         }
         if (!go)
             continue;
-        if (t.split) {
-            float4 *dst = reinterpret_cast<float4 *>(
-                p.part_o + ((static_cast<int64_t>(t.chunk) * p.n_rows * p.H) + id) * kHeadDim + 32 * half);
+        if (t.slot >= 0) {
+            float4 *dst = reinterpret_cast<float4 *>(p.part_o + part * kHeadDim + 32 * half);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
@@ -735,8 +711,8 @@ __device__ __forceinline__ void finish_cached_row(const CachedParams &p, uint32_
     }
     if (!go)
         return;
-    if (t.split)
-        p.part_ml[static_cast<int64_t>(t.chunk) * p.n_rows * p.H + id] = make_float2(m, l);
+    if (t.slot >= 0)
+        p.part_ml[part] = make_float2(m, l);
     else if (p.lse)
         p.lse[id] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
 }
@@ -927,10 +903,10 @@ __device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, cons
         }
         const int tok = r / p.group;
         const int64_t id = static_cast<int64_t>(w.row0 + tok) * p.H + w.hk * p.group + r - tok * p.group;
-        if (!VGGT_IN_RANGE(w.row0 + tok < p.n_rows && w.chunk < p.max_splits, kCheckAttnRow))
+        if (!VGGT_IN_RANGE(w.row0 + tok < p.n_rows && (w.slot < 0 || r < p.part_rows), kCheckAttnRow))
             continue;
-        if (w.split) {
-            const int64_t part = static_cast<int64_t>(w.chunk) * p.n_rows * p.H + id;
+        if (w.slot >= 0) {
+            const int64_t part = static_cast<int64_t>(w.slot) * p.part_rows + r;
             reinterpret_cast<float2 *>(p.part_o)[part * 32 + lane] = make_float2(a, b);
             if (lane == 0)
                 p.part_ml[part] = make_float2(top, sum);
@@ -1220,7 +1196,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         for (int i = 0; i < kTaskRing; ++i) {
             mbar_init(smem_u32(&sm.task_full[i]), 1);
-            mbar_init(smem_u32(&sm.task_empty[i]), 10);  // producer, issuer, eight softmax warps
+            mbar_init(smem_u32(&sm.task_empty[i]), 11);  // producers, issuer, eight softmax warps
         }
         mbar_init(smem_u32(&sm.merge_ready), 4);
         mbar_init(smem_u32(&sm.merge_free), 4);
@@ -1232,6 +1208,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(smem_u32(&sm.drain), 1);
         sm.ctl.abort = 0;
         sm.ctl.limit_ns = p.wait_limit_ns;
+        p.join[blockIdx.x] = Join{0, 0, 0, 0};  // what stays if a wait runs out
         fence_mbar_init();
         fence_proxy_async_smem();
     }
@@ -1244,23 +1221,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
         tmem_relinquish();
     }
-    plan_tasks(sm, p);
+    plan_work(sm, p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    const int n_tasks = sm.n_tasks, cta = static_cast<int>(blockIdx.x), ctas = static_cast<int>(gridDim.x);
-    const int my_tasks = n_tasks > cta ? (n_tasks - cta + ctas - 1) / ctas : 0;
 
     // 168 registers/thread at launch; 128 x (72 + 216 + 216) = 384 x 168.
     if (warp < 4) {
         setmaxnreg_dec<kRegsControl>();
         if (warp == 0)
-            run_cached_producer(sm, &tmQ, &tmK, &tmV, p);
+            run_cached_producer<false>(sm, &tmQ, &tmK, p);
         else if (warp == 1)
             run_cached_mma(sm, tmem);
         else if (warp == 2)
-            run_decoder(sm, p, my_tasks);
+            run_decoder(sm, p);
+        else
+            run_cached_producer<true>(sm, nullptr, &tmV, p);
     } else {
         setmaxnreg_inc<kRegsSoftmax>();
         run_cached_softmax(sm, tmem, p, (warp >> 2) - 1);
@@ -1275,82 +1252,47 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 }
 
-// Joins the parts of the rows whose keys were cut: O = sum_c 2^{m_c - M} O_c /
-// sum_c 2^{m_c - M} l_c, M = max m_c, in the order of the parts.  One warp per
-// row and head, two channels per lane.  Bound by latency and the parts' bytes.
+// Joins the parts of a unit that was cut, O = sum_c 2^{m_c - M} O_c / sum_c
+// 2^{m_c - M} l_c with M = max m_c, in the order of the parts.  Blocks x take
+// the unit that CTA x began, a warp a row at a time, two channels per lane.
+// Bound by latency (the launch waits for the attention's last CTA) and by the
+// parts' bytes, 264 per row and part.
+constexpr int kJoinRows = 32;  // rows of a block
 __global__ void __launch_bounds__(256) cached_combine_kernel(const CachedParams p)
 {
-    const int lane = threadIdx.x & 31;
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int64_t rows = static_cast<int64_t>(p.n_rows) * p.H;
-    int row = static_cast<int>(id / p.H), b = 0, parts = 1;
-    Seq s{0, 0, 0};
-    bool live = id < rows;
-    if (live) {
-        // The sequence of the row: the lanes look at 32 offsets at a time.
-        int lo = 0, hi = p.n_seqs;  // cu_rows[lo] <= row < cu_rows[hi], if row has a sequence
-        while (hi - lo > 1) {
-            const int step = (hi - lo + 31) / 32, at = min(lo + (lane + 1) * step, hi);
-            const unsigned over = __ballot_sync(0xffffffffu, at >= hi || __ldg(p.cu_rows + at) > row);
-            const int first = __ffs(over) - 1;  // at least lane 31's is over
-            hi = min(lo + (first + 1) * step, hi);
-            lo += first * step;
-        }
-        b = lo;
-        s = load_seq(p, b);
-        live = row >= s.row0 && row < s.row0 + s.n;
-    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!live)
+    const Join u = p.join[blockIdx.x];
+    if (u.parts == 0)
         return;
-    const int steps = p.header[0];
-    if (steps == kNoSplit)
-        return;
-    const int tiles = (s.n + p.tile_tokens - 1) / p.tile_tokens, tile = (row - s.row0) / p.tile_tokens;
-    if (tile < (tiles & ~1))
-        parts = parts_of(pair_tiles(p, s, tile >> 1), pair_step_tiles(steps));
-    else
-        parts = parts_of(key_tiles(p, s, s.n - 1), steps);
-    if (parts == 1)
-        return;  // written whole
-    float m[kMaxSplits / 32], l[kMaxSplits / 32], top = -INFINITY, sum = 0.f;
+    const int end = min(u.rows, static_cast<int>(blockIdx.y + 1) * kJoinRows);
+    for (int r = static_cast<int>(blockIdx.y) * kJoinRows + warp; r < end; r += 8) {
+        auto part = [&](int c) {
+            const int64_t slot = 2 * (static_cast<int64_t>(blockIdx.x) + c) + (c == 0);
+            return slot * p.part_rows + r;
+        };
+        float top = -INFINITY, sum = 0.f, o0 = 0.f, o1 = 0.f;
+        for (int c = lane; c < u.parts; c += 32)
+            top = fmaxf(top, p.part_ml[part(c)].x);
 #pragma unroll
-    for (int i = 0; i < kMaxSplits / 32; ++i) {
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane + 32 * i < parts)
-            ml = p.part_ml[(lane + 32 * i) * rows + id];
-        m[i] = ml.x;
-        l[i] = ml.y;
-        top = fmaxf(top, ml.x);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-#pragma unroll
-    for (int i = 0; i < kMaxSplits / 32; ++i) {
-        m[i] = m[i] == -INFINITY ? 0.f : ex2_approx(m[i] - top);  // now the part's weight
-        sum = fmaf(m[i], l[i], sum);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    float o0 = 0.f, o1 = 0.f;
-    const float2 *src = reinterpret_cast<const float2 *>(p.part_o) + id * (kHeadDim / 2) + lane;
-#pragma unroll
-    for (int i = 0; i < kMaxSplits / 32; ++i) {
-        const int here = min(32, parts - 32 * i);
+        for (int d = 16; d > 0; d >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
 #pragma unroll 4
-        for (int c = 0; c < here; ++c) {
-            const float w = __shfl_sync(0xffffffffu, m[i], c);
-            const float2 v = src[(32 * i + c) * rows * (kHeadDim / 2)];
-            o0 = fmaf(w, v.x, o0);
-            o1 = fmaf(w, v.y, o1);
+        for (int c = 0; c < u.parts; ++c) {
+            const int64_t at = part(c);
+            const float2 ml = p.part_ml[at], v = reinterpret_cast<const float2 *>(p.part_o)[at * 32 + lane];
+            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+            sum = fmaf(f, ml.y, sum);
+            o0 = fmaf(f, v.x, o0);
+            o1 = fmaf(f, v.y, o1);
         }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int tok = r / p.group;
+        const int64_t id = static_cast<int64_t>(u.row0 + tok) * p.H + u.hk * p.group + r - tok * p.group;
+        reinterpret_cast<uint32_t *>(p.o + id * kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
+        if (p.lse && lane == 0)
+            p.lse[id] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    reinterpret_cast<uint32_t *>(p.o + id * kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
-    if (p.lse && lane == 0)
-        p.lse[id] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
 }
 
 } // namespace vggt

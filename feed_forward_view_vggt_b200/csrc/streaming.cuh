@@ -173,35 +173,33 @@ VGGT_API vggt_status vggt_cache_append(vggt_cache cache, const void *k, const vo
 
 namespace {
 
-// Most parts a row's keys are split into.  With the fewest work items that
-// n_rows rows can make (pairs of 128-row tiles of one sequence), that many
-// parts give every SM about eight, whatever the lengths; 64 parts are enough
-// for one sequence of one key head.  Fixed by sizes alone, so that the
-// workspace size needs no device.
-int split_cap(const vggt_cache &c, int64_t n_rows)
+// Rows of a workspace slot: those of a pair of query tiles.
+int64_t part_rows(const vggt_cache &c, int64_t n_rows)
 {
-    const int64_t tiles = (static_cast<int64_t>(c.max_pages) * c.page_size + vggt::kBlockN - 1) / vggt::kBlockN;
-    const int64_t tokens = 2 * (vggt::kBlockM / (c.n_heads / c.n_kv_heads));
-    const int64_t items = c.n_kv_heads * ((n_rows + tokens - 1) / tokens);
-    int64_t cap = (8 * 148 + items - 1) / items;
-    cap = cap < 64 ? cap : 64;
-    return static_cast<int>(cap < tiles ? cap : tiles);
+    const int64_t group = c.n_heads / c.n_kv_heads, pair = 2 * (vggt::kBlockM / group);
+    return group * (n_rows < pair ? n_rows : pair);
 }
 
-// Workspace: 256 bytes of header, (m, l) of every part of every row and
-// head, float2 [cap][n_rows * H], and its sum of P V, float [cap][n_rows * H][64].
+// Workspace: one vggt::Join per CTA, (m, l) of every row of every slot,
+// float2 [2 * 148][part_rows], and its sum of P V, float [2 * 148][part_rows][64].
 struct CachedLayout {
     size_t ml, po, total;
 };
 
-CachedLayout cached_layout(const vggt_cache &c, int64_t n_rows, int cap)
+CachedLayout cached_layout(const vggt_cache &c, int64_t n_rows)
 {
-    const size_t rows = static_cast<size_t>(n_rows) * c.n_heads;
+    const size_t rows = 2 * static_cast<size_t>(vggt::kMaxCtas) * static_cast<size_t>(part_rows(c, n_rows));
     CachedLayout l;
-    l.ml = 256;
-    l.po = align256(l.ml + cap * rows * 8);
-    l.total = align256(l.po + cap * rows * vggt::kHeadDim * 4);
+    l.ml = align256(vggt::kMaxCtas * sizeof(vggt::Join));
+    l.po = align256(l.ml + rows * 8);
+    l.total = align256(l.po + rows * vggt::kHeadDim * 4);
     return l;
+}
+
+// Key tiles of the longest sequence that the block table can hold.
+int64_t most_key_tiles(const vggt_cache &c)
+{
+    return (static_cast<int64_t>(c.max_pages) * c.page_size + vggt::kBlockN - 1) / vggt::kBlockN;
 }
 
 // Query rows [n_rows, H, 64] with their strides; a box holds the G heads of
@@ -246,10 +244,7 @@ bool make_pages_map(CUtensorMap *map, const void *pages, const vggt_cache &c, in
 
 VGGT_API size_t vggt_attn_cached_workspace_bytes(vggt_cache cache, int32_t n_rows)
 {
-    if (check_cache(cache) != VGGT_OK || n_rows < 1)
-        return 0;
-    const int cap = split_cap(cache, n_rows);
-    return cap > 1 ? cached_layout(cache, n_rows, cap).total : 0;
+    return check_cache(cache) != VGGT_OK || n_rows < 1 ? 0 : cached_layout(cache, n_rows).total;
 }
 
 VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q_row_stride, int64_t q_head_stride,
@@ -274,7 +269,7 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     if (!q || !o || !aligned16(q) || !aligned16(o) || !aligned4(lse))
         return VGGT_ERR_INVALID_ARG;
     const size_t need = vggt_attn_cached_workspace_bytes(cache, n_rows);
-    if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
         return VGGT_ERR_INVALID_ARG;
     if (workspace_bytes < need)
         return VGGT_ERR_WORKSPACE;
@@ -310,7 +305,12 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     p.box_rows = cache.page_size & -cache.page_size;
     if (p.box_rows > vggt::kBlockN)
         p.box_rows = vggt::kBlockN;
-    p.max_splits = need > 0 ? split_cap(cache, n_rows) : 1;
+    // The most that the units can cost: every unit as a pair of tiles over the longest sequence.
+    const int64_t units = cache.n_kv_heads * ((n_rows + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens) +
+                                              static_cast<int64_t>(cache.n_seqs));
+    const int64_t most = 2 * most_key_tiles(cache) + vggt::kUnitCost;
+    while ((units * ((most >> p.cost_shift) + 1)) > INT32_MAX)
+        ++p.cost_shift;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.table = block_table;
     p.cu_rows = cu_rows;
@@ -318,20 +318,20 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.lse = lse;
     p.wait_limit_ns = vggt::kWaitLimitNs;
-    if (need > 0) {
-        const CachedLayout l = cached_layout(cache, n_rows, p.max_splits);
-        uint8_t *ws = static_cast<uint8_t *>(workspace);
-        p.header = reinterpret_cast<int32_t *>(ws);
-        p.part_ml = reinterpret_cast<float2 *>(ws + l.ml);
-        p.part_o = reinterpret_cast<float *>(ws + l.po);
-    }
+    const CachedLayout l = cached_layout(cache, n_rows);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    p.part_rows = static_cast<int>(part_rows(cache, n_rows));
+    p.join = reinterpret_cast<vggt::Join *>(ws);
+    p.part_ml = reinterpret_cast<float2 *>(ws + l.ml);
+    p.part_o = reinterpret_cast<float *>(ws + l.po);
     CUtensorMap tq, tk, tv;
     if (!make_query_map(&tq, q, cache, n_rows, q_row_stride, q_head_stride, p.group, p.tile_tokens) ||
         !make_pages_map(&tk, k_pages, cache, p.box_rows) || !make_pages_map(&tv, v_pages, cache, p.box_rows))
         return VGGT_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    vggt::cached_attn_kernel<<<num_sms, vggt::kAttnThreads, vggt::cached_smem_bytes(cache.n_seqs), s>>>(tq, tk, tv, p);
-    if ((st = launched()) != VGGT_OK || p.max_splits == 1)
+    const unsigned grid = static_cast<unsigned>(num_sms < vggt::kMaxCtas ? num_sms : vggt::kMaxCtas);
+    vggt::cached_attn_kernel<<<grid, vggt::kAttnThreads, vggt::cached_smem_bytes(cache.n_seqs), s>>>(tq, tk, tv, p);
+    if ((st = launched()) != VGGT_OK || most_key_tiles(cache) == 1)  // one key tile: nothing to cut
         return st;
     // The joining launch is set up while the attention runs and waits for its
     // end on the device.
@@ -340,7 +340,7 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + 7) / 8));
+    cfg.gridDim = dim3(grid, static_cast<unsigned>((p.part_rows + vggt::kJoinRows - 1) / vggt::kJoinRows));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cfg.attrs = &attr;
