@@ -62,6 +62,28 @@ constexpr int kSoftmaxWarps = 8;  // and with how many: 16 keys of a tile each
 enum : uint32_t { kSiteTaskFull = 12, kSiteTaskEmpty, kSiteMergeReady, kSiteMergeFree, kSiteFewQ, kSiteFewFull, kSiteTaskPassed };
 enum : int { kTaskSingle = 0, kTaskPair = 1, kTaskFew = 2 };
 
+// x / d for 0 <= x < 2^31 by a multiplication (the planning is a chain of
+// divisions, and nothing else runs while its first tasks are found): with
+// 2^(k-1) < d <= 2^k and mul = floor(2^(31+k) / d) + 1, mul d exceeds 2^(31+k)
+// by at most d <= 2^k, which moves the quotient of no x < 2^31.
+struct Divisor {
+    uint32_t d, mul, shift;
+
+    void set(uint32_t value)
+    {
+        d = value;
+        uint32_t k = 0;
+        while ((uint64_t{1} << k) < value)
+            ++k;
+        shift = k > 0 ? k - 1 : 0;
+        mul = k > 0 ? static_cast<uint32_t>((uint64_t{1} << (31 + k)) / value + 1) : 0;
+    }
+    __device__ __forceinline__ int div(int x) const
+    {
+        return d == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), mul) >> shift);
+    }
+};
+
 // What a CTA leaves for the joining launch: the unit whose first part, but not
 // its last, was its work.  Parts 1, 2, ... are those of the CTAs behind it.
 struct Join {
@@ -71,6 +93,7 @@ struct Join {
 struct CachedParams {
     int n_seqs, n_rows, H, Hkv, group, tile_tokens;  // group G = H / Hkv, tile_tokens F
     int page_size, n_pages, max_pages, unit, box_rows;
+    Divisor by_group, by_tile, by_page, by_unit;
     int cost_shift;  // costs are counted in 2^cost_shift steps, so that their sum fits in 31 bits
     int part_rows;   // rows of a workspace slot
     float scale_log2;
@@ -136,20 +159,20 @@ __device__ __forceinline__ Seq load_seq(const CachedParams &p, int b)
 }
 
 // Keys that the row of position pos sees.  pos + unit fits in 32 unsigned bits.
-__device__ __forceinline__ int key_limit(int kv, int pos, int unit)
+__device__ __forceinline__ int key_limit(const CachedParams &p, int kv, int pos)
 {
-    if (unit == 0)
+    if (p.unit == 0)
         return kv;
     if (pos < 0)
         return 0;
-    const unsigned u = static_cast<unsigned>(unit), lim = (static_cast<unsigned>(pos) / u + 1u) * u;
+    const unsigned lim = (static_cast<unsigned>(p.by_unit.div(pos)) + 1u) * static_cast<unsigned>(p.unit);
     return static_cast<int>(min(static_cast<unsigned>(kv), lim));
 }
 
 // Key tiles that rows 0 .. i of a sequence see (the limit never falls with the row).
 __device__ __forceinline__ int key_tiles(const CachedParams &p, const Seq &s, int i)
 {
-    return (key_limit(s.kv, s.kv - s.n + i, p.unit) + kBlockN - 1) / kBlockN;
+    return (key_limit(p, s.kv, s.kv - s.n + i) + kBlockN - 1) / kBlockN;
 }
 
 // Key tiles of query-tile pair pr.
@@ -161,7 +184,7 @@ __device__ __forceinline__ int pair_tiles(const CachedParams &p, const Seq &s, i
 // The units of one key head of a sequence: pairs first, then the single tile.
 __device__ __forceinline__ int unit_count(const CachedParams &p, const Seq &s)
 {
-    return ((s.n + p.tile_tokens - 1) / p.tile_tokens + 1) >> 1;
+    return (p.by_tile.div(s.n + p.tile_tokens - 1) + 1) >> 1;
 }
 
 struct Unit {
@@ -260,7 +283,7 @@ __device__ __forceinline__ void write_empty_rows(const CachedParams &p, int row0
     const int lane = threadIdx.x & 31;
     const int rows = min(row_end - row0, (kind == kTaskPair ? 2 : 1) * p.tile_tokens) * p.group;
     for (int i = lane >> 3; i < rows; i += 4) {
-        const int tok = i / p.group;
+        const int tok = p.by_group.div(i);
         const int64_t id = static_cast<int64_t>(row0 + tok) * p.H + hk * p.group + i - tok * p.group;
         reinterpret_cast<uint4 *>(p.o + id * kHeadDim)[lane & 7] = make_uint4(0u, 0u, 0u, 0u);
         if (p.lse && (lane & 7) == 0)
@@ -274,13 +297,18 @@ __device__ __forceinline__ void write_empty_rows(const CachedParams &p, int row0
 __device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &p)
 {
     const int lane = threadIdx.x & 31, cta = static_cast<int>(blockIdx.x);
-    const int64_t work = sm.work;
-    const int64_t ctas = max(int64_t{1}, min(static_cast<int64_t>(gridDim.x), (work << p.cost_shift) / kMinSteps));
+    const int work = sm.work;
+    const int ctas = work >= kMaxCtas * kMinSteps
+                         ? static_cast<int>(gridDim.x)
+                         : max(1, min(static_cast<int>(gridDim.x), (work << p.cost_shift) / kMinSteps));
+    // CTA i starts at floor(i * work / ctas)
+    const int each = work / ctas, rest = work - each * ctas;
+    auto start = [&](int i) { return i * each + i * rest / ctas; };
     Join join{0, 0, 0, 0};
     int w = 0, w1 = 0;
     if (cta < ctas) {
-        w = static_cast<int>(cta * work / ctas);
-        w1 = static_cast<int>((cta + 1) * work / ctas);
+        w = start(cta);
+        w1 = start(cta + 1);
     }
     uint32_t it = 0;
     auto push = [&](const Task &t) -> bool {
@@ -343,11 +371,14 @@ __device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &
                     t.slot = 2 * cta + (t.kt0 == 0);
                     if (t.kt0 == 0) {
                         // up to the CTA that has the unit's last point
-                        const int64_t end = static_cast<int64_t>(w) - x + u.cost;
+                        const int end = w - x + u.cost;
+                        int last = min(ctas - 1, static_cast<int>(static_cast<float>(end) * ctas / work) + 1);
+                        while (last > cta && start(last) >= end)
+                            --last;
                         join.row0 = t.row0;
                         join.rows = min(t.row_end - t.row0, 2 * p.tile_tokens) * p.group;
                         join.hk = hk;
-                        join.parts = static_cast<int>((end * ctas + work - 1) / work) - cta;
+                        join.parts = last - cta + 1;
                     }
                 }
                 if (t.n > 0 && !push(t))
@@ -413,13 +444,12 @@ __device__ __forceinline__ void run_cached_producer(CachedSmem &sm, const CUtens
                 const int valid = j == n - 1 ? vlast : kBlockN;
                 if (lane * p.box_rows >= valid)
                     return 0;
-                const int page = __ldg(table + ((kt0 + j) * kBlockN + lane * p.box_rows) / p.page_size);
+                const int page = __ldg(table + p.by_page.div((kt0 + j) * kBlockN + lane * p.box_rows));
                 if (page >= 0 && page < p.n_pages)
                     return page;
                 record_bounds_failure(kCheckCachePage);
                 return p.n_pages;  // outside the map: the box is filled with zeros
             };
-            int page = lookup(0);
             if (!kIsV) {
                 const int qb = it & 1;
                 if (!wait_bar_warp(smem_u32(&sm.q_empty[qb]), ((static_cast<uint32_t>(it) >> 1) & 1) ^ 1, ab, kSiteQEmpty))
@@ -432,10 +462,11 @@ __device__ __forceinline__ void run_cached_producer(CachedSmem &sm, const CUtens
                                     row0 + p.tile_tokens);
                 }
             }
+            int page = lookup(0);
             for (int j = 0; j < n; ++j) {
                 const int valid = j == n - 1 ? vlast : kBlockN;
                 const int boxes = (valid + p.box_rows - 1) / p.box_rows;
-                const int off = ((kt0 + j) * kBlockN + lane * p.box_rows) % p.page_size;
+                const int key = (kt0 + j) * kBlockN + lane * p.box_rows, off = key - p.by_page.div(key) * p.page_size;
                 const int here = page;
                 if (j + 1 < n)
                     page = lookup(j + 1);
@@ -719,10 +750,12 @@ __device__ __forceinline__ void finish_cached_row(const CachedParams &p, uint32_
 
 // A task of at most 16 rows (a single token of grouped heads, the last tokens
 // of a chunk) needs 1/8 of a 128-row tile's arithmetic and is bound by the
-// bytes of K and V, so it does without TMEM: warp w takes keys 16 w .. 16 w +
-// 15 of every key tile with 16 x 8 x 16 products on registers, keeps its own
-// softmax state and follows the K/V ring by itself; the eight states meet once,
-// at the end of the task, in the Q buffer.  Fragment layouts are those of
+// bytes of K and V, so it does without TMEM: the even key tiles belong to warps
+// 0-3 and the odd ones to warps 4-7, 32 keys of a tile to each warp.  A warp
+// multiplies on registers (16 x 8 x 16), keeps its own softmax state and
+// follows the K/V ring by itself; the eight states meet once, at the end of the
+// task, in the Q buffer.  (With 16 keys of every tile to each of the eight
+// warps, the chain of a tile, 1280 clocks, was as long as its bytes take.)  Fragment layouts are those of
 // ldmatrix and mma.m16n8k16: row g = lane / 4 (and g + 8), columns 2 (lane % 4)
 // and the next.
 __device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, const Task &w, uint32_t it, uint32_t ring,
@@ -734,6 +767,7 @@ __device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, cons
     uint8_t *qbuf = sm.q[qb][0];
     const float sl2 = p.scale_log2;
     const int rows = (w.row_end - w.row0) * p.group;
+    const int mine = 32 * (warp & 3), half = warp >> 2;  // this warp's keys of a tile, its tiles mod 2
     int lim[2];  // keys that rows g, g + 8 see, counted from this warp's first key
     int low = 0x7fffffff;
 #pragma unroll
@@ -741,12 +775,12 @@ __device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, cons
         const int r = g + 8 * e;
         lim[e] = 0;
         if (r < rows) {
-            lim[e] = key_limit(w.kv, w.pos0 + r / p.group, p.unit) - w.kt0 * kBlockN - 16 * warp;
+            lim[e] = key_limit(p, w.kv, w.pos0 + p.by_group.div(r)) - w.kt0 * kBlockN - mine;
             low = min(low, lim[e]);
         }
     }
     low = __reduce_min_sync(0xffffffffu, low);
-    const int all = w.kv - w.kt0 * kBlockN - 16 * warp;  // keys that exist, counted in the same way
+    const int all = w.kv - w.kt0 * kBlockN - mine;  // keys that exist, counted in the same way
 
     if (!wait_bar_warp(smem_u32(&sm.task_passed[it % (2 * kTaskRing)]), (it / (2 * kTaskRing)) & 1u, ab,
                        kSiteTaskPassed) ||
@@ -769,33 +803,40 @@ __device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, cons
         for (int e = 0; e < 4; ++e)
             o[i][e] = 0.f;
     // Byte offsets within a tile; the swizzle XORs a 16-byte column with the row's low 3 bits.
-    const int k_row = 16 * warp + (lane & 7), v_row = 16 * warp + (lane & 15);
-    const uint32_t k_off = k_row * 128, v_off = v_row * 128;
-    for (int j = 0; j < w.n; ++j) {
+    const uint32_t k_off = (mine + (lane & 7)) * 128, v_off = (mine + (lane & 15)) * 128;
+    uint32_t k_at[2], v_at[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        k_at[i] = smem_u32(sm.k[0]) + k_off + (((4 * i + (lane >> 3)) ^ (lane & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v_at[i] = smem_u32(sm.v[0]) + v_off + (((2 * i + (lane >> 4)) ^ (lane & 7)) << 4);
+    for (int j = half; j < w.n; j += 2) {
         const uint32_t u = ring + static_cast<uint32_t>(j), st = u % kStages, ph = (u / kStages) & 1u;
-        const int here = all - j * kBlockN;  // keys of this warp's 16 that exist
+        const int here = all - j * kBlockN;  // keys of this warp's 32 that exist
         if (!wait_bar_warp(smem_u32(&sm.k_full[st]), ph, ab, kSiteKFull))
             return false;
-        float s[2][4] = {};
+        float s[4][4] = {};
         if (here > 0) {
-            uint32_t k[4][4];  // [key half][d half]: two 16-channel steps of B
-            const uint32_t base = smem_u32(sm.k[st]) + k_off;
+            uint32_t k[4][2][4];  // [8 keys][32 channels]: two 16-channel steps of B each
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                ldmatrix_x4(base + (i >> 1) * 1024 + (((4 * (i & 1) + (lane >> 3)) ^ (lane & 7)) << 4), k[i]);
+#pragma unroll
+                for (int d = 0; d < 2; ++d)
+                    ldmatrix_x4(k_at[d] + st * kTileBytes + i * 1024, k[i][d]);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    mma_16816(s[i], q[kk], k[2 * i + (kk >> 1)][2 * (kk & 1)], k[2 * i + (kk >> 1)][2 * (kk & 1) + 1]);
+                for (int i = 0; i < 4; ++i)
+                    mma_16816(s[i], q[kk], k[i][kk >> 1][2 * (kk & 1)], k[i][kk >> 1][2 * (kk & 1) + 1]);
         }
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(smem_u32(&sm.k_empty[st]));
+            mbar_arrive_n(smem_u32(&sm.k_empty[st]), 2);  // for its counterpart of the other half too
         if (here > 0) {
-            if (low < (j + 1) * kBlockN) {  // some row may not see all of the 16 keys
+            if (low < j * kBlockN + 32) {  // some row may not see all of the 32 keys
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (8 * i + c2 + (e & 1) >= lim[e >> 1] - j * kBlockN)
@@ -803,8 +844,12 @@ __device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, cons
             }
             float top[2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                top[e] = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1])) * sl2;
+            for (int e = 0; e < 2; ++e) {
+                top[e] = fmax3(s[0][2 * e], s[0][2 * e + 1], s[1][2 * e]);
+                top[e] = fmax3(top[e], s[1][2 * e + 1], s[2][2 * e]);
+                top[e] = fmax3(top[e], s[2][2 * e + 1], s[3][2 * e]);
+                top[e] = fmaxf(top[e], s[3][2 * e + 1]) * sl2;
+            }
             // The offset moves when a logit passes it by kRescaleThreshold
             // (P <= 2^8), so most tiles need no maximum over the lanes.
             if (__any_sync(0xffffffffu, top[0] > m[0] + kRescaleThreshold || top[1] > m[1] + kRescaleThreshold)) {
@@ -822,49 +867,61 @@ __device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, cons
                     }
                 }
             }
-            uint32_t pk[4];
+            uint32_t pk[2][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const float base = m[e] == -INFINITY ? 0.f : m[e];
+                float sum[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     const float a = ex2_approx(fmaf(s[i][2 * e], sl2, -base));
                     const float b = ex2_approx(fmaf(s[i][2 * e + 1], sl2, -base));
-                    l[e] += a + b;
-                    pk[2 * i + e] = pack_bf16x2(a, b);
+                    sum[i & 1] = i < 2 ? a + b : sum[i & 1] + (a + b);
+                    pk[i >> 1][2 * (i & 1) + e] = pack_bf16x2(a, b);
                 }
+                l[e] += sum[0] + sum[1];
             }
             if (!wait_bar_warp(smem_u32(&sm.v_full[st]), ph, ab, kSiteVFull))
                 return false;
-            const uint32_t base = smem_u32(sm.v[st]) + v_off;
+            uint32_t v[2][4][4];  // [16 keys][16 channels]
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t v[4];
-                ldmatrix_x4_trans(base + (((2 * i + (lane >> 4)) ^ (lane & 7)) << 4), v);
-                if (here < 16) {
-                    // whatever lies behind the last key must not meet P = 0
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ldmatrix_x4_trans(v_at[i] + st * kTileBytes + h * 2048, v[h][i]);
+            if (here < 32) {
+                // whatever lies behind the last key must not meet P = 0
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int key = 8 * (e & 1) + c2;
-                        v[e] &= (key < here ? 0x0000ffffu : 0u) | (key + 1 < here ? 0xffff0000u : 0u);
+                        const int key = 16 * h + 8 * (e & 1) + c2;
+                        const uint32_t keep = (key < here ? 0x0000ffffu : 0u) | (key + 1 < here ? 0xffff0000u : 0u);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[h][i][e] &= keep;
                     }
-                }
-                mma_16816(o[2 * i], pk, v[0], v[1]);
-                mma_16816(o[2 * i + 1], pk, v[2], v[3]);
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mma_16816(o[2 * i], pk[h], v[h][i][0], v[h][i][1]);
+                    mma_16816(o[2 * i + 1], pk[h], v[h][i][2], v[h][i][3]);
+                }
         } else if (!wait_bar_warp(smem_u32(&sm.v_full[st]), ph, ab, kSiteVFull)) {
             return false;
         }
         __syncwarp();
         if (lane == 0)
-            mbar_arrive(smem_u32(&sm.v_empty[st]));
+            mbar_arrive_n(smem_u32(&sm.v_empty[st]), 2);
     }
 
     // The states of the eight warps, over Q once every warp has read it:
     // [warp][row][64] floats, pairs of columns XORed with the row against bank conflicts.
     if (!wait_bar_warp(smem_u32(&sm.few_q), fews & 1u, ab, kSiteFewQ))
         return false;
-    float2 *mine = reinterpret_cast<float2 *>(qbuf) + warp * (kFewRows * 32);
+    float2 *state = reinterpret_cast<float2 *>(qbuf) + warp * (kFewRows * 32);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -874,7 +931,7 @@ __device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, cons
             sm.merge_ml[warp * kFewRows + r] = make_float2(m[e], l[e]);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            mine[r * 32 + ((4 * i + (lane & 3)) ^ (g << 2))] = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+            state[r * 32 + ((4 * i + (lane & 3)) ^ (g << 2))] = make_float2(o[i][2 * e], o[i][2 * e + 1]);
     }
     __syncwarp();
     if (lane == 0)
@@ -901,7 +958,7 @@ __device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, cons
             a = fmaf(f, v.x, a);
             b = fmaf(f, v.y, b);
         }
-        const int tok = r / p.group;
+        const int tok = p.by_group.div(r);
         const int64_t id = static_cast<int64_t>(w.row0 + tok) * p.H + w.hk * p.group + r - tok * p.group;
         if (!VGGT_IN_RANGE(w.row0 + tok < p.n_rows && (w.slot < 0 || r < p.part_rows), kCheckAttnRow))
             continue;
@@ -940,7 +997,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
     const uint64_t neg_one2 = f2_pack(-1.f, -1.f);
     const uint64_t c0_2 = f2_pack(kExp2C0, kExp2C0), c1_2 = f2_pack(kExp2C1, kExp2C1);
     const uint64_t c2_2 = f2_pack(kExp2C2, kExp2C2), c3_2 = f2_pack(kExp2C3, kExp2C3);
-    const int tok = t / p.group, tile_head = t - tok * p.group;
+    const int tok = p.by_group.div(t), tile_head = t - tok * p.group;
     uint32_t k0 = 0;         // steps of the CTA before the task
     uint32_t ring = 0;       // key tiles before the task
     uint32_t c = 0;          // steps of this warpgroup
@@ -973,7 +1030,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
         const int head = w.hk * p.group + tile_head;
         const int steps = w.kind == kTaskPair ? w.n : (w.n + 1 - wg) >> 1;  // of this warpgroup
         // keys this row sees, counted from the task's first key
-        const int lim = row_ok ? key_limit(w.kv, w.pos0 + tile_tok, p.unit) - w.kt0 * kBlockN : 0;
+        const int lim = row_ok ? key_limit(p, w.kv, w.pos0 + tile_tok) - w.kt0 * kBlockN : 0;
         const bool warp_ok = __any_sync(0xffffffffu, row_ok);
         const int warp_lim = __reduce_min_sync(0xffffffffu, row_ok ? lim : 0x7fffffff);
         float m = -INFINITY, l = 0.f;
@@ -1272,22 +1329,53 @@ __global__ void __launch_bounds__(256) cached_combine_kernel(const CachedParams 
             return slot * p.part_rows + r;
         };
         float top = -INFINITY, sum = 0.f, o0 = 0.f, o1 = 0.f;
-        for (int c = lane; c < u.parts; c += 32)
-            top = fmaxf(top, p.part_ml[part(c)].x);
+        // The first parts' values are on their way while the weights are found.
+        constexpr int kAhead = 12;
+        float2 v[kAhead];
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c)
+            if (c < u.parts)
+                v[c] = reinterpret_cast<const float2 *>(p.part_o)[part(c) * 32 + lane];
+        constexpr int kSets = (kMaxCtas + 31) / 32;
+        float f[kSets], l[kSets];  // of parts lane, lane + 32, ...: the offset, then the weight; the sum
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            const float2 ml = lane + 32 * i < u.parts ? p.part_ml[part(lane + 32 * i)] : make_float2(-INFINITY, 0.f);
+            f[i] = ml.x;
+            l[i] = ml.y;
+            top = fmaxf(top, ml.x);
+        }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-#pragma unroll 4
-        for (int c = 0; c < u.parts; ++c) {
-            const int64_t at = part(c);
-            const float2 ml = p.part_ml[at], v = reinterpret_cast<const float2 *>(p.part_o)[at * 32 + lane];
-            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
-            sum = fmaf(f, ml.y, sum);
-            o0 = fmaf(f, v.x, o0);
-            o1 = fmaf(f, v.y, o1);
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            f[i] = f[i] == -INFINITY ? 0.f : ex2_approx(f[i] - top);
+            sum = fmaf(f[i], l[i], sum);
         }
+#pragma unroll
+        for (int c = 0; c < kAhead; ++c) {
+            const float w = __shfl_sync(0xffffffffu, f[0], c);
+            if (c < u.parts) {
+                o0 = fmaf(w, v[c].x, o0);
+                o1 = fmaf(w, v[c].y, o1);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+#pragma unroll 4
+            for (int c = max(kAhead, 32 * i); c < min(u.parts, 32 * i + 32); ++c) {
+                const float w = __shfl_sync(0xffffffffu, f[i], c & 31);
+                const float2 x = reinterpret_cast<const float2 *>(p.part_o)[part(c) * 32 + lane];
+                o0 = fmaf(w, x.x, o0);
+                o1 = fmaf(w, x.y, o1);
+            }
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, d);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int tok = r / p.group;
+        const int tok = p.by_group.div(r);
         const int64_t id = static_cast<int64_t>(u.row0 + tok) * p.H + u.hk * p.group + r - tok * p.group;
         reinterpret_cast<uint32_t *>(p.o + id * kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
         if (p.lse && lane == 0)

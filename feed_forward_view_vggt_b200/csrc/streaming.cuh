@@ -302,6 +302,10 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     p.n_pages = cache.n_pages;
     p.max_pages = cache.max_pages;
     p.unit = causal_unit;
+    p.by_group.set(static_cast<uint32_t>(p.group));
+    p.by_tile.set(static_cast<uint32_t>(p.tile_tokens));
+    p.by_page.set(static_cast<uint32_t>(p.page_size));
+    p.by_unit.set(static_cast<uint32_t>(causal_unit > 0 ? causal_unit : 1));
     p.box_rows = cache.page_size & -cache.page_size;
     if (p.box_rows > vggt::kBlockN)
         p.box_rows = vggt::kBlockN;
