@@ -392,7 +392,7 @@ __device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &
             }
         }
     }
-    if (lane == 0)
+    if (lane == 0 && p.join)
         p.join[cta] = join;
     push(Task{});
 }
@@ -1265,7 +1265,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         mbar_init(smem_u32(&sm.drain), 1);
         sm.ctl.abort = 0;
         sm.ctl.limit_ns = p.wait_limit_ns;
-        p.join[blockIdx.x] = Join{0, 0, 0, 0};  // what stays if a wait runs out
+        if (p.join)
+            p.join[blockIdx.x] = Join{0, 0, 0, 0};  // what stays if a wait runs out
         fence_mbar_init();
         fence_proxy_async_smem();
     }

@@ -244,7 +244,10 @@ bool make_pages_map(CUtensorMap *map, const void *pages, const vggt_cache &c, in
 
 VGGT_API size_t vggt_attn_cached_workspace_bytes(vggt_cache cache, int32_t n_rows)
 {
-    return check_cache(cache) != VGGT_OK || n_rows < 1 ? 0 : cached_layout(cache, n_rows).total;
+    // one key tile: no unit can be cut
+    if (check_cache(cache) != VGGT_OK || n_rows < 1 || most_key_tiles(cache) == 1)
+        return 0;
+    return cached_layout(cache, n_rows).total;
 }
 
 VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q_row_stride, int64_t q_head_stride,
@@ -269,7 +272,7 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     if (!q || !o || !aligned16(q) || !aligned16(o) || !aligned4(lse))
         return VGGT_ERR_INVALID_ARG;
     const size_t need = vggt_attn_cached_workspace_bytes(cache, n_rows);
-    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    if (need > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)))
         return VGGT_ERR_INVALID_ARG;
     if (workspace_bytes < need)
         return VGGT_ERR_WORKSPACE;
@@ -322,12 +325,14 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     p.o = static_cast<__nv_bfloat16 *>(o);
     p.lse = lse;
     p.wait_limit_ns = vggt::kWaitLimitNs;
-    const CachedLayout l = cached_layout(cache, n_rows);
-    uint8_t *ws = static_cast<uint8_t *>(workspace);
-    p.part_rows = static_cast<int>(part_rows(cache, n_rows));
-    p.join = reinterpret_cast<vggt::Join *>(ws);
-    p.part_ml = reinterpret_cast<float2 *>(ws + l.ml);
-    p.part_o = reinterpret_cast<float *>(ws + l.po);
+    if (need > 0) {
+        const CachedLayout l = cached_layout(cache, n_rows);
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        p.part_rows = static_cast<int>(part_rows(cache, n_rows));
+        p.join = reinterpret_cast<vggt::Join *>(ws);
+        p.part_ml = reinterpret_cast<float2 *>(ws + l.ml);
+        p.part_o = reinterpret_cast<float *>(ws + l.po);
+    }
     CUtensorMap tq, tk, tv;
     if (!make_query_map(&tq, q, cache, n_rows, q_row_stride, q_head_stride, p.group, p.tile_tokens) ||
         !make_pages_map(&tk, k_pages, cache, p.box_rows) || !make_pages_map(&tv, v_pages, cache, p.box_rows))
@@ -335,7 +340,7 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const unsigned grid = static_cast<unsigned>(num_sms < vggt::kMaxCtas ? num_sms : vggt::kMaxCtas);
     vggt::cached_attn_kernel<<<grid, vggt::kAttnThreads, vggt::cached_smem_bytes(cache.n_seqs), s>>>(tq, tk, tv, p);
-    if ((st = launched()) != VGGT_OK || most_key_tiles(cache) == 1)  // one key tile: nothing to cut
+    if ((st = launched()) != VGGT_OK || need == 0)
         return st;
     // The joining launch is set up while the attention runs and waits for its
     // end on the device.
