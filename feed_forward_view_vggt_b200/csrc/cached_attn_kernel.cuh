@@ -28,8 +28,8 @@
 //
 // CTA (384 threads, one per SM): warps 0 and 3 load Q and K, and V, by TMA, page
 // by page (a 4-D map of the pages; a box is the largest power of two of rows
-// that divides the page, at most 128), warp 1 issues the UMMAs, warp 2 walks
-// along the CTA's work and writes its tasks into a ring, warps 4-7 and 8-11 are the softmax warpgroups.
+// that divides the page, at most 128); warp 0 also walks along the CTA's work
+// and writes its tasks into a ring; warps 1 and 2 issue the UMMAs; warps 4-7 and 8-11 are the softmax warpgroups.
 // TMEM, score buffers and the order S(k+3) after PV(k) are those of
 // attn_fwd_kernel.
 //
@@ -125,12 +125,12 @@ struct __align__(1024) CachedSmem {
     uint64_t k_full[kStages], k_empty[kStages];
     uint64_t v_full[kStages], v_empty[kStages];
     uint64_t s_full[2][3], p_ready[2][3];  // by warpgroup and its step count mod 3
-    uint64_t o_done[2], o_final[2];
+    uint64_t buf_free[kScoreBufs], o_final[2];
     uint64_t merge_ready, merge_free;
     uint64_t few_q, few_full[2];  // by tasks of few rows mod 2
-    uint64_t task_passed[2 * kTaskRing];  // the issuer has done with the task
+    uint64_t task_passed[2 * kTaskRing];  // the issuers are past the task
     uint64_t task_full[kTaskRing], task_empty[kTaskRing];
-    uint64_t drain;
+    uint64_t drain[2];
     uint32_t tmem_base;
     WaitCtl ctl;
     int work;
@@ -291,10 +291,104 @@ __device__ __forceinline__ void write_empty_rows(const CachedParams &p, int row0
     }
 }
 
-// Warp 2: walks along the CTA's part of the work and hands on its tasks, then
-// one with n = 0 that ends the list.  Units without keys (their sequence was
+// Reads task `it` from the ring (the caller releases it once read).
+__device__ __forceinline__ bool wait_task(CachedSmem &sm, int it)
+{
+    return wait_bar(smem_u32(&sm.task_full[it % kTaskRing]), (static_cast<uint32_t>(it) / kTaskRing) & 1, &sm.ctl,
+                    kSiteTaskFull);
+}
+
+__device__ __forceinline__ void release_task(CachedSmem &sm, int it)
+{
+    mbar_arrive(smem_u32(&sm.task_empty[it % kTaskRing]));
+}
+
+// Copies in flight of a producer warp: uses of the K (or V) ring, Q tiles.
+struct Issued {
+    uint32_t tiles, q;
+};
+
+// Loads the K (with Q before it) or the V tiles of a task; false when a wait
+// ran out.  Page by page: lane i copies the i-th box of a tile.
+template <bool kIsV>
+__device__ __forceinline__ bool load_task(CachedSmem &sm, const CUtensorMap *tmQ, const CUtensorMap *tmKV,
+                                          const CachedParams &p, const Task &t, Issued &issued)
+{
+    volatile WaitCtl *ab = &sm.ctl;
+    const int lane = threadIdx.x & 31;
+    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * kHeadDim * 2;
+    const uint32_t full = smem_u32(kIsV ? sm.v_full : sm.k_full), empty = smem_u32(kIsV ? sm.v_empty : sm.k_empty);
+    const uint32_t tiles = smem_u32(kIsV ? sm.v[0] : sm.k[0]);
+    const int n = t.n, hk = t.hk, kt0 = t.kt0, vlast = t.vlast;
+    const int32_t *table = p.table + static_cast<int64_t>(t.b) * p.max_pages;
+    if (!kIsV) {
+        const uint32_t qb = issued.q & 1u, q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * kHeadDim * 2;
+        if (!wait_bar_warp(smem_u32(&sm.q_empty[qb]), ((issued.q >> 1) & 1u) ^ 1u, ab, kSiteQEmpty))
+            return false;
+        if (lane == 0) {
+            const bool pair = t.kind == kTaskPair;
+            mbar_arrive_expect_tx(smem_u32(&sm.q_full[qb]), pair ? 2 * q_bytes : q_bytes);
+            tma_load_3d(smem_u32(sm.q[qb][0]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group, t.row0);
+            if (pair)
+                tma_load_3d(smem_u32(sm.q[qb][1]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group,
+                            t.row0 + p.tile_tokens);
+        }
+        ++issued.q;
+    }
+    // Page of this lane's box of tile j; the first key of the box exists.
+    auto lookup = [&](int j) -> int {
+        const int valid = j == n - 1 ? vlast : kBlockN;
+        if (lane * p.box_rows >= valid)
+            return 0;
+        const int page = __ldg(table + p.by_page.div((kt0 + j) * kBlockN + lane * p.box_rows));
+        if (page >= 0 && page < p.n_pages)
+            return page;
+        record_bounds_failure(kCheckCachePage);
+        return p.n_pages;  // outside the map: the box is filled with zeros
+    };
+    int page = lookup(0);
+    for (int j = 0; j < n; ++j) {
+        const int valid = j == n - 1 ? vlast : kBlockN;
+        const int boxes = (valid + p.box_rows - 1) / p.box_rows;
+        const int key = (kt0 + j) * kBlockN + lane * p.box_rows, off = key - p.by_page.div(key) * p.page_size;
+        const int here = page;
+        if (j + 1 < n)
+            page = lookup(j + 1);
+        const uint32_t st = issued.tiles % kStages;
+        if (!wait_bar_warp(empty + 8 * st, ((issued.tiles / kStages) & 1u) ^ 1u, ab, kIsV ? kSiteVEmpty : kSiteKEmpty))
+            return false;
+        if (lane == 0)
+            mbar_arrive_expect_tx(full + 8 * st, boxes * box_bytes);
+        ++issued.tiles;
+        __syncwarp();
+        if (lane < boxes)
+            tma_load_4d(tiles + st * kTileBytes + lane * box_bytes, tmKV, full + 8 * st, 0, off, hk, here);
+    }
+    return true;
+}
+
+// Every copy that the warp started must land before the CTA may exit.
+template <bool kIsV>
+__device__ __forceinline__ void drain_copies(CachedSmem &sm, const Issued &issued)
+{
+    const uint32_t full = smem_u32(kIsV ? sm.v_full : sm.k_full);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        for (uint32_t i = (issued.tiles > kStages ? issued.tiles - kStages : 0); i < issued.tiles; ++i)
+            wait_drain(full + 8 * (i % kStages), (i / kStages) & 1);
+        for (uint32_t i = (issued.q > 2 ? issued.q - 2 : 0); i < issued.q; ++i)
+            wait_drain(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1);
+    }
+    __syncwarp();
+}
+
+// Warp 0: walks along the CTA's part of the work, hands on its tasks, then one
+// with n = 0 that ends the list, and loads their Q and K tiles.  V is warp 3's:
+// the copies of a tile of small pages are many (16 of 2 KB for pages of 16),
+// and a warp issues those of its lanes one after another.  Units without keys (their sequence was
 // refused pages, e.g.) are dealt with here and never enter the ring.
-__device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &p)
+__device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ, const CUtensorMap *tmK,
+                                          const CachedParams &p, Issued &issued)
 {
     const int lane = threadIdx.x & 31, cta = static_cast<int>(blockIdx.x);
     const int work = sm.work;
@@ -321,7 +415,7 @@ __device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &
         }
         __syncwarp();
         ++it;
-        return true;
+        return t.n == 0 || load_task<false>(sm, tmQ, tmK, p, t, issued);
     };
     while (w < w1) {
         // The sequence, head and unit at point w, and x, its place in the unit.
@@ -397,198 +491,51 @@ __device__ __forceinline__ void run_decoder(CachedSmem &sm, const CachedParams &
     push(Task{});
 }
 
-// Reads task `it` from the ring (the caller releases it once read).
-__device__ __forceinline__ bool wait_task(CachedSmem &sm, int it)
+__device__ __forceinline__ void run_k_producer(CachedSmem &sm, const CUtensorMap *tmQ, const CUtensorMap *tmK,
+                                               const CachedParams &p)
 {
-    return wait_bar(smem_u32(&sm.task_full[it % kTaskRing]), (static_cast<uint32_t>(it) / kTaskRing) & 1, &sm.ctl,
-                    kSiteTaskFull);
+    Issued issued{0, 0};
+    walk_work(sm, tmQ, tmK, p, issued);
+    drain_copies<false>(sm, issued);
 }
 
-__device__ __forceinline__ void release_task(CachedSmem &sm, int it)
+__device__ __forceinline__ void run_v_producer(CachedSmem &sm, const CUtensorMap *tmV, const CachedParams &p)
 {
-    mbar_arrive(smem_u32(&sm.task_empty[it % kTaskRing]));
-}
-
-// Warp 0 loads Q and K, warp 3 V: the copies of a tile of small pages are many
-// (16 of 2 KB for pages of 16), and a warp issues those of its lanes one after
-// another.
-template <bool kIsV>
-__device__ __forceinline__ void run_cached_producer(CachedSmem &sm, const CUtensorMap *tmQ, const CUtensorMap *tmKV,
-                                                    const CachedParams &p)
-{
-    volatile WaitCtl *ab = &sm.ctl;
-    const int lane = threadIdx.x & 31;
-    const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * kHeadDim * 2;
-    const uint32_t q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * kHeadDim * 2;
-    const uint32_t full = smem_u32(kIsV ? sm.v_full : sm.k_full), empty = smem_u32(kIsV ? sm.v_empty : sm.k_empty);
-    const uint32_t tiles = smem_u32(kIsV ? sm.v[0] : sm.k[0]);
-    uint32_t issued = 0;
-    int it = 0;
-    for (;; ++it) {
+    Issued issued{0, 0};
+    for (int it = 0;; ++it) {
         const bool got = wait_task(sm, it);
         __syncwarp();
         if (!__all_sync(0xffffffffu, got))
-            goto out;
-        {
-            const Task &tr = sm.task[it % kTaskRing];
-            const int n = tr.n, hk = tr.hk, row0 = tr.row0, kt0 = tr.kt0, vlast = tr.vlast;
-            const bool pair = tr.kind == kTaskPair;
-            const int32_t *table = p.table + static_cast<int64_t>(tr.b) * p.max_pages;
-            __syncwarp();
-            if (lane == 0)
-                release_task(sm, it);
-            if (n == 0)
-                goto out;
-            // Page of this lane's box of tile j; the first key of the box exists.
-            auto lookup = [&](int j) -> int {
-                const int valid = j == n - 1 ? vlast : kBlockN;
-                if (lane * p.box_rows >= valid)
-                    return 0;
-                const int page = __ldg(table + p.by_page.div((kt0 + j) * kBlockN + lane * p.box_rows));
-                if (page >= 0 && page < p.n_pages)
-                    return page;
-                record_bounds_failure(kCheckCachePage);
-                return p.n_pages;  // outside the map: the box is filled with zeros
-            };
-            if (!kIsV) {
-                const int qb = it & 1;
-                if (!wait_bar_warp(smem_u32(&sm.q_empty[qb]), ((static_cast<uint32_t>(it) >> 1) & 1) ^ 1, ab, kSiteQEmpty))
-                    goto out;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(smem_u32(&sm.q_full[qb]), pair ? 2 * q_bytes : q_bytes);
-                    tma_load_3d(smem_u32(sm.q[qb][0]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group, row0);
-                    if (pair)
-                        tma_load_3d(smem_u32(sm.q[qb][1]), tmQ, smem_u32(&sm.q_full[qb]), 0, hk * p.group,
-                                    row0 + p.tile_tokens);
-                }
-            }
-            int page = lookup(0);
-            for (int j = 0; j < n; ++j) {
-                const int valid = j == n - 1 ? vlast : kBlockN;
-                const int boxes = (valid + p.box_rows - 1) / p.box_rows;
-                const int key = (kt0 + j) * kBlockN + lane * p.box_rows, off = key - p.by_page.div(key) * p.page_size;
-                const int here = page;
-                if (j + 1 < n)
-                    page = lookup(j + 1);
-                const uint32_t st = issued % kStages;
-                if (!wait_bar_warp(empty + 8 * st, ((issued / kStages) & 1) ^ 1, ab, kIsV ? kSiteVEmpty : kSiteKEmpty)) {
-                    ++it;
-                    goto out;
-                }
-                if (lane == 0)
-                    mbar_arrive_expect_tx(full + 8 * st, boxes * box_bytes);
-                ++issued;
-                __syncwarp();
-                if (lane < boxes)
-                    tma_load_4d(tiles + st * kTileBytes + lane * box_bytes, tmKV, full + 8 * st, 0, off, hk, here);
-            }
-        }
+            break;
+        const Task t = sm.task[it % kTaskRing];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            release_task(sm, it);
+        if (t.n == 0 || !load_task<true>(sm, nullptr, tmV, p, t, issued))
+            break;
     }
-out:
-    // Every copy this warp started must land before the CTA may exit; `it` is
-    // the number of Q tiles.
-    __syncwarp();
-    if (lane == 0) {
-        for (uint32_t i = (issued > kStages ? issued - kStages : 0); i < issued; ++i)
-            wait_drain(full + 8 * (i % kStages), (i / kStages) & 1);
-        for (int i = (it > 2 ? it - 2 : 0); !kIsV && i < it; ++i)
-            wait_drain(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1);
-    }
-    __syncwarp();
+    drain_copies<true>(sm, issued);
 }
 
-// The issuer has left task `it` behind; for one of few rows this means that
-// all products of the tasks before it are complete.  The warps wait for that
-// before they follow the K/V ring themselves: a warp that had no step in some
-// single tiles would otherwise take an older phase of a ring barrier for the
-// one it waits for (as would an issuer that is ahead of the warps, see fews_over).  Twice the slots of the task ring keep the phases of
-// these barriers apart: the issuer has left task it - 16 when task it appears
-// in the ring, and cannot reach task it + 16 before the warps release task it + 8.
+// The two issuers, one thread each: warp 2 issues S = Q K^T, warp 1 O += P V
+// (one thread for both took 1450 clocks per step with every barrier it waited
+// for complete: the loop itself was the bound).  Step k of the CTA uses score
+// buffer k % 3: S(k + 3) waits for PV(k), so the scores are up to three steps
+// ahead.  Within a task step s belongs to warpgroup s & 1, and to key tile s /
+// 2 (pair) or s (single).
+//
+// A task of few rows is passed: the warps read its tiles themselves.  Whoever
+// follows a ring barrier without waiting for every phase of it must not run
+// ahead of one: the warps start on such a task when both issuers have passed it
+// (then all loads before it are complete; a warp may have had no step in some
+// single tiles), and an issuer goes on to the next task for the tensor cores
+// when the warps are done (fews_over).  Twice the slots of the task ring keep
+// the phases of `task_passed` apart: an issuer has left task it - 16 when task
+// it appears in the ring, and cannot reach it + 16 before the warps release it + 8.
 __device__ __forceinline__ void pass_task(CachedSmem &sm, int it)
 {
     mbar_arrive(smem_u32(&sm.task_passed[it % (2 * kTaskRing)]));
 }
-
-// Position of the issuer in the steps of this CTA's tasks.  Within a task
-// step s belongs to warpgroup s & 1, and to key tile s / 2 (pair) or s (single).
-struct TaskCursor {
-    int it, s, steps;   // task, step within it, its steps
-    int kind;           // of the task; -1: the end of the tasks, or a wait ran out
-    int kk_last;        // PV products of 16 keys in its last key tile
-    uint32_t st, ph;    // K/V ring stage and its phase
-    uint32_t buf;       // score buffer
-    uint32_t c0, c1;    // steps of each warpgroup so far
-    uint32_t fews, fews_done;  // tasks of few rows passed, and those known to be over (fews or one less)
-
-    // Reads task `it`; true if it is one of the issuer's.
-    template <bool kRelease>
-    __device__ __forceinline__ bool open(CachedSmem &sm)
-    {
-        kind = -1;
-        if (!wait_task(sm, it))
-            return false;
-        const Task &t = sm.task[it % kTaskRing];
-        const int n = t.n;
-        if (n > 0)
-            kind = t.kind;
-        kk_last = (t.vlast + 15) >> 4;
-        if (kRelease)
-            release_task(sm, it);
-        steps = kind == kTaskPair ? 2 * n : n;
-        s = 0;
-        return kind == kTaskSingle || kind == kTaskPair;
-    }
-
-    // Passes a task of few rows, whose key tiles the warps read themselves.
-    // The warps may start on it while they still work on the one before.
-    __device__ __forceinline__ bool pass(CachedSmem &sm)
-    {
-        pass_task(sm, it);
-        const uint32_t x = st + static_cast<uint32_t>(steps);
-        ph ^= (x / kStages) & 1u;
-        st = x % kStages;
-        ++it;
-        return fews_over(sm) && (++fews, open<true>(sm) || kind == kTaskFew);
-    }
-
-    // Waits until the warps have done with the tasks of few rows passed so
-    // far: then every ring barrier is in the phase that the cursor has it in.
-    __device__ __forceinline__ bool fews_over(CachedSmem &sm)
-    {
-        if (fews_done == fews)
-            return true;
-        if (!wait_bar(smem_u32(&sm.few_full[fews_done & 1u]), (fews_done >> 1) & 1u, &sm.ctl, kSiteFewFull))
-            return false;
-        ++fews_done;
-        return true;
-    }
-
-    __device__ __forceinline__ uint32_t wg() const { return static_cast<uint32_t>(s) & 1u; }
-    __device__ __forceinline__ uint32_t count() const { return wg() ? c1 : c0; }
-    __device__ __forceinline__ bool last_reader() const { return kind == kTaskSingle || wg(); }
-    __device__ __forceinline__ bool first_reader() const { return kind == kTaskSingle || !wg(); }
-
-    // Moves to the next step; false if the next task is not the issuer's.
-    template <bool kRelease>
-    __device__ __forceinline__ bool next(CachedSmem &sm)
-    {
-        if (last_reader() && ++st == kStages) {
-            st = 0;
-            ph ^= 1u;
-        }
-        if (wg())
-            ++c1;
-        else
-            ++c0;
-        buf = buf == kScoreBufs - 1 ? 0u : buf + 1;
-        if (++s < steps)
-            return true;
-        if (kRelease)
-            pass_task(sm, it);
-        ++it;
-        return open<kRelease>(sm);
-    }
-};
 
 // A ring barrier that the warps release with one arrival each; the issuer
 // stands for all of them, with its last arrival when the products are done.
@@ -598,98 +545,130 @@ __device__ __forceinline__ void commit_release(uint32_t bar)
     umma_commit(bar);
 }
 
-__device__ __forceinline__ void issue_score(CachedSmem &sm, uint32_t tmem, const TaskCursor &c, const TileDescs &td)
-{
-    constexpr uint32_t kIdescS = idesc_bf16_f32(kBlockM, kBlockN, false);
-    const uint32_t qb = static_cast<uint32_t>(c.it) & 1u;
-    const uint64_t a = td.q0 + (2 * qb + (c.kind == kTaskPair ? c.wg() : 0u)) * kTileDescStep, b = td.k0 + c.st * kTileDescStep;
-    const uint32_t d = tmem + c.buf * kBlockN;
-#pragma unroll
-    for (int kk = 0; kk < kHeadDim / 16; ++kk)
-        umma_ss(d, a + 2 * kk, b + 2 * kk, kIdescS, kk > 0 ? 1u : 0u);
-    umma_commit(smem_u32(&sm.s_full[c.wg()][c.count() % 3]));
-    if (c.last_reader())
-        commit_release(smem_u32(&sm.k_empty[c.st]));
-    if (c.s == c.steps - 1)
-        commit_release(smem_u32(&sm.q_empty[qb]));
-}
+// Slot and phase of barriers that are used in turn.
+template <uint32_t kSlots>
+struct Turn {
+    uint32_t slot, ph;
 
-__device__ __forceinline__ bool score_ready(CachedSmem &sm, const TaskCursor &c)
-{
-    if (c.s == 0 && !wait_bar(smem_u32(&sm.q_full[static_cast<uint32_t>(c.it) & 1u]), (static_cast<uint32_t>(c.it) >> 1) & 1u, &sm.ctl, kSiteQFull))
-        return false;
-    return !c.first_reader() || wait_bar(smem_u32(&sm.k_full[c.st]), c.ph, &sm.ctl, kSiteKFull);
-}
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == kSlots) {
+            slot = 0;
+            ph ^= 1u;
+        }
+    }
+};
 
-__device__ __forceinline__ void cached_mma_loop(CachedSmem &sm, uint32_t tmem)
+template <bool kIsPV>
+__device__ __forceinline__ void issue_loop(CachedSmem &sm, uint32_t tmem)
 {
-    constexpr uint32_t kIdescPV = idesc_bf16_f32(kBlockM, kHeadDim, true);
     volatile WaitCtl *ab = &sm.ctl;
-    const TileDescs td{sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024), sdesc_sw128(smem_u32(sm.k[0]), 16, 1024),
-                       sdesc_sw128(smem_u32(sm.v[0]), 16, 1024)};
-    TaskCursor vc{};  // next PV to issue
-    vc.open<true>(sm);
-    for (;;) {
-        while (vc.kind == kTaskFew)
-            if (!vc.pass(sm))
-                return;
-        if (vc.kind < 0 || !vc.fews_over(sm))
+    const uint64_t q0 = sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
+    const uint64_t kv0 = sdesc_sw128(smem_u32(kIsPV ? sm.v[0] : sm.k[0]), 16, 1024);
+    const uint32_t full = smem_u32(kIsPV ? sm.v_full : sm.k_full), empty = smem_u32(kIsPV ? sm.v_empty : sm.k_empty);
+    const uint32_t mine = smem_u32(kIsPV ? sm.p_ready[0] : sm.s_full[0]);  // [wg][turn]
+    const uint32_t freed = smem_u32(sm.buf_free);
+    Turn<kStages> ring{0, 0};
+    Turn<kScoreBufs> buf{0, 0}, turn{0, 0}, other{0, 0};  // of the step's warpgroup and of the other one
+    uint32_t fews = 0, fews_done = 0;  // tasks of few rows passed, and those known to be over (fews or one less)
+    auto fews_over = [&]() -> bool {
+        if (fews_done == fews)
+            return true;
+        ++fews_done;
+        return wait_bar(smem_u32(&sm.few_full[(fews_done - 1) & 1u]), ((fews_done - 1) >> 1) & 1u, ab, kSiteFewFull);
+    };
+    for (int it = 0;; ++it) {
+        if (!wait_task(sm, it))
             return;
-        // A run of tasks for the tensor cores: the next S is up to three
-        // steps ahead, but never past a task of few rows.  (Looking further
-        // would mean waiting for tasks behind a ring full of those.)
-        TaskCursor sc = vc;  // next S to issue
-        bool s_more = true, v_more = true;
-        for (int i = 0; i < kScoreBufs && s_more; ++i) {
-            if (!score_ready(sm, sc))
+        const Task &t = sm.task[it % kTaskRing];
+        const int n = t.n, kind = t.kind, kk_last = (t.vlast + 15) >> 4;
+        release_task(sm, it);
+        if (n == 0)
+            return;
+        if (kind == kTaskFew) {
+            // the warps may start on it while they still work on the one before
+            pass_task(sm, it);
+            if (!fews_over())
                 return;
-            tc_fence_after();
-            issue_score(sm, tmem, sc, td);
-            s_more = sc.next<false>(sm);
+            ++fews;
+            const uint32_t x = ring.slot + static_cast<uint32_t>(n);
+            ring.ph ^= (x / kStages) & 1u;
+            ring.slot = x % kStages;
+            continue;
         }
-        while (v_more) {
-            const uint32_t wg = vc.wg(), c = vc.count();
-            if (vc.first_reader() && !wait_bar(smem_u32(&sm.v_full[vc.st]), vc.ph, ab, kSiteVFull))
+        if (!fews_over())
+            return;
+        const bool pair = kind == kTaskPair;
+        const int steps = pair ? 2 * n : n, last_tile = pair ? steps - 2 : steps - 1;
+        const uint32_t qb = static_cast<uint32_t>(it) & 1u;
+        if (!kIsPV && !wait_bar(smem_u32(&sm.q_full[qb]), (static_cast<uint32_t>(it) >> 1) & 1u, ab, kSiteQFull))
+            return;
+        for (int s = 0; s < steps; ++s) {
+            const uint32_t wg = static_cast<uint32_t>(s) & 1u;
+            const bool first_reader = !pair || !wg, last_reader = !pair || wg;
+            if (first_reader && !wait_bar(full + 8 * ring.slot, ring.ph, ab, kIsPV ? kSiteVFull : kSiteKFull))
                 return;
-            if (!wait_bar(smem_u32(&sm.p_ready[wg][c % 3]), (c / 3) & 1u, ab, kSitePReady))
-                return;
-            tc_fence_after();
-            const uint64_t b = td.v0 + vc.st * kTileDescStep;
-            const uint32_t d = tmem + kTmemO + wg * kHeadDim, a = tmem + vc.buf * kBlockN;
-            const bool last = vc.kind == kTaskPair ? vc.s >= vc.steps - 2 : vc.s == vc.steps - 1;  // the last key tile
-            const int kks = last ? vc.kk_last : kBlockN / 16;
-#pragma unroll
-            for (int kk = 0; kk < kBlockN / 16; ++kk)
-                if (kk < kks)
-                    umma_ts(d, a + 8 * kk, b + 128 * kk, kIdescPV, (vc.s >= 2 || kk > 0) ? 1u : 0u);
-            umma_commit(smem_u32(&sm.o_done[wg]));
-            if (vc.s >= vc.steps - 2)  // the warpgroup's last step of the task
-                umma_commit(smem_u32(&sm.o_final[wg]));
-            if (vc.last_reader())
-                commit_release(smem_u32(&sm.v_empty[vc.st]));
-            v_more = vc.next<true>(sm);
-            if (s_more && !score_ready(sm, sc))
-                return;
-            // S(k + 3) overwrites the buffer PV(k) reads P from.  Waited for
-            // behind the run's last S too: the next run starts on free buffers.
-            if (!wait_bar(smem_u32(&sm.o_done[wg]), c & 1u, ab, kSiteODone))
-                return;
-            if (s_more) {
+            const uint32_t bar = mine + 8 * (3 * wg + turn.slot);
+            const uint64_t b = kv0 + ring.slot * kTileDescStep;
+            const uint32_t scores = tmem + buf.slot * kBlockN;
+            if (kIsPV) {
+                constexpr uint32_t kIdesc = idesc_bf16_f32(kBlockM, kHeadDim, true);
+                if (!wait_bar(bar, turn.ph, ab, kSitePReady))
+                    return;
                 tc_fence_after();
-                issue_score(sm, tmem, sc, td);
-                s_more = sc.next<false>(sm);
+                const uint32_t d = tmem + kTmemO + wg * kHeadDim;
+                umma_ts(d, scores, b, kIdesc, s >= 2 ? 1u : 0u);
+                if (s < last_tile) {
+#pragma unroll
+                    for (int kk = 1; kk < kBlockN / 16; ++kk)
+                        umma_ts(d, scores + 8 * kk, b + 128 * kk, kIdesc, 1u);
+                } else {
+                    for (int kk = 1; kk < kk_last; ++kk)
+                        umma_ts(d, scores + 8 * kk, b + 128 * kk, kIdesc, 1u);
+                }
+                umma_commit(freed + 8 * buf.slot);
+                if (s >= steps - 2)  // the warpgroup's last step of the task
+                    umma_commit(smem_u32(&sm.o_final[wg]));
+            } else {
+                constexpr uint32_t kIdesc = idesc_bf16_f32(kBlockM, kBlockN, false);
+                if (!wait_bar(freed + 8 * buf.slot, buf.ph ^ 1u, ab, kSiteODone))
+                    return;
+                tc_fence_after();
+                const uint64_t a = q0 + (2 * qb + (pair ? wg : 0u)) * kTileDescStep;
+#pragma unroll
+                for (int kk = 0; kk < kHeadDim / 16; ++kk)
+                    umma_ss(scores, a + 2 * kk, b + 2 * kk, kIdesc, kk > 0 ? 1u : 0u);
+                umma_commit(bar);
             }
+            if (last_reader) {
+                commit_release(empty + 8 * ring.slot);
+                ring.next();
+            }
+            buf.next();
+            turn.next();
+            const Turn<kScoreBufs> x = turn;
+            turn = other;
+            other = x;
         }
+        if (steps & 1) {  // the next task starts with warpgroup 0 again
+            const Turn<kScoreBufs> x = turn;
+            turn = other;
+            other = x;
+        }
+        if (!kIsPV)
+            commit_release(smem_u32(&sm.q_empty[qb]));
+        pass_task(sm, it);
     }
 }
 
-__device__ __forceinline__ void run_cached_mma(CachedSmem &sm, uint32_t tmem)
+template <bool kIsPV>
+__device__ __forceinline__ void run_issuer(CachedSmem &sm, uint32_t tmem)
 {
     if (elect_one()) {
-        cached_mma_loop(sm, tmem);
+        issue_loop<kIsPV>(sm, tmem);
         // Every UMMA issued must complete before TMEM is released.
-        umma_commit(smem_u32(&sm.drain));
-        wait_drain(smem_u32(&sm.drain), 0);
+        umma_commit(smem_u32(&sm.drain[kIsPV]));
+        wait_drain(smem_u32(&sm.drain[kIsPV]), 0);
     }
     __syncwarp();
 }
@@ -758,7 +737,7 @@ __device__ __forceinline__ void finish_cached_row(const CachedParams &p, uint32_
 // warps, the chain of a tile, 1280 clocks, was as long as its bytes take.)  Fragment layouts are those of
 // ldmatrix and mma.m16n8k16: row g = lane / 4 (and g + 8), columns 2 (lane % 4)
 // and the next.
-__device__ __noinline__ bool run_few(CachedSmem &sm, const CachedParams &p, const Task &w, uint32_t it, uint32_t ring,
+__device__ __forceinline__ bool run_few(CachedSmem &sm, const CachedParams &p, const Task &w, uint32_t it, uint32_t ring,
                                      uint32_t fews, int warp)
 {
     volatile WaitCtl *ab = &sm.ctl;
@@ -989,7 +968,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
     const uint32_t lane_off = static_cast<uint32_t>((t >> 5) * 32) << 16;
     const uint32_t tO = tmem + kTmemO + static_cast<uint32_t>(wg * kHeadDim) + lane_off;
     const uint32_t bar_s = smem_u32(&sm.s_full[wg][0]), bar_p = smem_u32(&sm.p_ready[wg][0]);
-    const uint32_t bar_o = smem_u32(&sm.o_done[wg]), bar_of = smem_u32(&sm.o_final[wg]);
+    const uint32_t bar_of = smem_u32(&sm.o_final[wg]);
     const float sl2 = p.scale_log2;
     const uint64_t sl2_2 = f2_pack(sl2, sl2);
     const uint64_t magic2 = f2_pack(kRoundMagic, kRoundMagic);
@@ -998,9 +977,9 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
     const uint64_t c0_2 = f2_pack(kExp2C0, kExp2C0), c1_2 = f2_pack(kExp2C1, kExp2C1);
     const uint64_t c2_2 = f2_pack(kExp2C2, kExp2C2), c3_2 = f2_pack(kExp2C3, kExp2C3);
     const int tok = p.by_group.div(t), tile_head = t - tok * p.group;
-    uint32_t k0 = 0;         // steps of the CTA before the task
+    uint32_t k0 = 0;         // steps of the CTA before the task, mod 6 (3 score buffers, 2 phases)
     uint32_t ring = 0;       // key tiles before the task
-    uint32_t c = 0;          // steps of this warpgroup
+    Turn<3> turn{0, 0};      // barriers of this warpgroup's step
     uint32_t finals = 0;     // tasks in which it had a step
     uint32_t fews = 0;       // tasks of few rows so far
     uint32_t merges = 0;     // single-tile tasks that both warpgroups worked on
@@ -1035,11 +1014,14 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
         const int warp_lim = __reduce_min_sync(0xffffffffu, row_ok ? lim : 0x7fffffff);
         float m = -INFINITY, l = 0.f;
 
-        for (int x = 0; x < steps; ++x, ++c) {
+        uint32_t k = k0 + static_cast<uint32_t>(wg);  // the step, mod 6
+        for (int x = 0; x < steps; ++x) {
             const int j = w.kind == kTaskPair ? x : 2 * x + wg;  // key tile within the task
-            const uint32_t buf = (k0 + static_cast<uint32_t>(2 * x + wg)) % kScoreBufs;
+            if (k >= 6)
+                k -= 6;
+            const uint32_t buf = k >= 3 ? k - 3 : k;
             const uint32_t tS = tmem + buf * kBlockN + lane_off;
-            if (!wait_bar_warp(bar_s + 8 * (c % 3), (c / 3) & 1, ab, kSiteSFull))
+            if (!wait_bar_warp(bar_s + 8 * turn.slot, turn.ph, ab, kSiteSFull))
                 return;
             if (j == w.n - 1 && (w.vlast & 15) != 0 && (w.kind != kTaskPair || wg == 0)) {
                 // V rows behind the last key, up to the end of its group of 16
@@ -1137,7 +1119,10 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
                     const float cand = tile_max();
                     const bool need = cand > m + kRescaleThreshold;
                     if (__any_sync(0xffffffffu, need)) {
-                        if (!wait_bar_warp(bar_o, (c - 1) & 1, ab, kSiteODone))
+                        // this warpgroup's last PV: step k - 2
+                        const uint32_t before = k >= 2 ? k - 2 : k + 4;
+                        if (!wait_bar_warp(smem_u32(&sm.buf_free[before >= 3 ? before - 3 : before]), before >= 3,
+                                           ab, kSiteODone))
                             return;
                         tc_fence_after();
                         const float f = need ? ex2_approx(m - cand) : 1.f;
@@ -1173,9 +1158,11 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
             tc_fence_before();
             __syncwarp();
             if ((threadIdx.x & 31) == 0)
-                mbar_arrive(bar_p + 8 * (c % 3));
+                mbar_arrive(bar_p + 8 * turn.slot);
+            turn.next();
+            k += 2;
         }
-        k0 += static_cast<uint32_t>(w.kind == kTaskPair ? 2 * w.n : w.n);
+        k0 = (k0 + static_cast<uint32_t>(w.kind == kTaskPair ? 2 * w.n : w.n)) % 6;
         ring += static_cast<uint32_t>(w.n);
 
         if (steps == 0)
@@ -1242,7 +1229,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 mbar_init(smem_u32(&sm.s_full[i][c]), 1);
                 mbar_init(smem_u32(&sm.p_ready[i][c]), 4);
             }
-            mbar_init(smem_u32(&sm.o_done[i]), 1);
+            mbar_init(smem_u32(&sm.drain[i]), 1);
             mbar_init(smem_u32(&sm.o_final[i]), 1);
         }
         for (int i = 0; i < kStages; ++i) {
@@ -1253,7 +1240,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         for (int i = 0; i < kTaskRing; ++i) {
             mbar_init(smem_u32(&sm.task_full[i]), 1);
-            mbar_init(smem_u32(&sm.task_empty[i]), 11);  // producers, issuer, eight softmax warps
+            mbar_init(smem_u32(&sm.task_empty[i]), 11);  // V producer, issuers, eight softmax warps
         }
         mbar_init(smem_u32(&sm.merge_ready), 4);
         mbar_init(smem_u32(&sm.merge_free), 4);
@@ -1261,8 +1248,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         for (int i = 0; i < 2; ++i)
             mbar_init(smem_u32(&sm.few_full[i]), kSoftmaxWarps);
         for (int i = 0; i < 2 * kTaskRing; ++i)
-            mbar_init(smem_u32(&sm.task_passed[i]), 1);
-        mbar_init(smem_u32(&sm.drain), 1);
+            mbar_init(smem_u32(&sm.task_passed[i]), 2);
+        for (int i = 0; i < kScoreBufs; ++i)
+            mbar_init(smem_u32(&sm.buf_free[i]), 1);
         sm.ctl.abort = 0;
         sm.ctl.limit_ns = p.wait_limit_ns;
         if (p.join)
@@ -1289,13 +1277,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (warp < 4) {
         setmaxnreg_dec<kRegsControl>();
         if (warp == 0)
-            run_cached_producer<false>(sm, &tmQ, &tmK, p);
+            run_k_producer(sm, &tmQ, &tmK, p);
         else if (warp == 1)
-            run_cached_mma(sm, tmem);
+            run_issuer<true>(sm, tmem);
         else if (warp == 2)
-            run_decoder(sm, p);
+            run_issuer<false>(sm, tmem);
         else
-            run_cached_producer<true>(sm, nullptr, &tmV, p);
+            run_v_producer(sm, &tmV, p);
     } else {
         setmaxnreg_inc<kRegsSoftmax>();
         run_cached_softmax(sm, tmem, p, (warp >> 2) - 1);
