@@ -51,6 +51,10 @@
 namespace vggt {
 
 constexpr int kMaxCtas = 148;
+// Of every 16 column pairs of a score row, those whose exponentials are a
+// polynomial (see attn_fwd_kernel, which takes 4).  Measured, one frame over
+// 100 cached: 0: 967 us, 1: 973, 2: 959, 3: 948, 4: 969, 5: 1060, 6: 1160.
+constexpr int kCachedPolyPairs = 3;
 constexpr int kTaskRing = 8;
 // What a unit costs beside its steps (Q load, first score, epilogue), in
 // steps, and the fewest steps a CTA is used for.
@@ -961,6 +965,16 @@ __device__ __forceinline__ bool run_few(CachedSmem &sm, const CachedParams &p, c
     return true;
 }
 
+// wait_bar_warp for the step's own barrier, with one vote where the phase is complete.
+__device__ __forceinline__ bool wait_step(uint32_t bar, uint32_t parity, volatile WaitCtl *ctl, uint32_t site)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        return true;
+    const bool ok = wait_slow(bar, parity, ctl, site);
+    __syncwarp();
+    return __all_sync(0xffffffffu, ok);
+}
+
 __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem, const CachedParams &p, int wg)
 {
     volatile WaitCtl *ab = &sm.ctl;
@@ -1021,7 +1035,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
                 k -= 6;
             const uint32_t buf = k >= 3 ? k - 3 : k;
             const uint32_t tS = tmem + buf * kBlockN + lane_off;
-            if (!wait_bar_warp(bar_s + 8 * turn.slot, turn.ph, ab, kSiteSFull))
+            if (!wait_step(bar_s + 8 * turn.slot, turn.ph, ab, kSiteSFull))
                 return;
             if (j == w.n - 1 && (w.vlast & 15) != 0 && (w.kind != kTaskPair || wg == 0)) {
                 // V rows behind the last key, up to the end of its group of 16
@@ -1082,7 +1096,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
                                 f2_pack(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), sl2_2, neg_m2);
                             float a, b;
                             f2_unpack(x2, a, b);
-                            if (e < kExp2PolyPairs) {
+                            if (e < kCachedPolyPairs) {
                                 const uint64_t xc = f2_pack(fmaxf(a, kExp2MinArg), fmaxf(b, kExp2MinArg));
                                 const uint64_t y = f2_add(xc, magic2);
                                 const uint64_t jj = f2_add(y, neg_magic2);
@@ -1149,7 +1163,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
                 l += tsum;
                 tmem_st_wait();
             }
-            if (merge_open) {
+            if (x == 0 && merge_open) {
                 // warpgroup 0 still reads this warpgroup's O of an earlier task
                 if (!wait_bar_warp(smem_u32(&sm.merge_free), (merges - 1) & 1, ab, kSiteMergeFree))
                     return;
@@ -1300,76 +1314,75 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
 // Joins the parts of a unit that was cut, O = sum_c 2^{m_c - M} O_c / sum_c
 // 2^{m_c - M} l_c with M = max m_c, in the order of the parts.  Blocks x take
-// the unit that CTA x began, a warp a row at a time, two channels per lane.
-// Bound by latency (the launch waits for the attention's last CTA) and by the
-// parts' bytes, 264 per row and part.
-constexpr int kJoinRows = 32;  // rows of a block
+// the unit that CTA x began; 16 threads a row, four channels each.  Bound by
+// latency (the launch waits for the attention's last CTA, then for the record,
+// the weights and the values) and by the parts' bytes, 264 per row and part.
+// The first kAhead values are on their way while the weights are found: with
+// few rows a unit can have many parts, with many rows the registers count.
+constexpr int kJoinRows = 16;  // rows of a block
+template <int kAhead>
 __global__ void __launch_bounds__(256) cached_combine_kernel(const CachedParams p)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 15, r = static_cast<int>(blockIdx.y) * kJoinRows + (threadIdx.x >> 4);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Join u = p.join[blockIdx.x];
-    if (u.parts == 0)
+    if (static_cast<int>(blockIdx.y) * kJoinRows >= u.rows || u.parts == 0)
         return;
-    const int end = min(u.rows, static_cast<int>(blockIdx.y + 1) * kJoinRows);
-    for (int r = static_cast<int>(blockIdx.y) * kJoinRows + warp; r < end; r += 8) {
-        auto part = [&](int c) {
-            const int64_t slot = 2 * (static_cast<int64_t>(blockIdx.x) + c) + (c == 0);
-            return slot * p.part_rows + r;
+    const bool live = r < u.rows;
+    // Row r of part c: slot 2 x + 1 for the first, 2 (x + c) for the others.
+    const int64_t step = 2 * static_cast<int64_t>(p.part_rows);
+    const int64_t base = step * blockIdx.x + (live ? r : 0);
+    auto row = [&](int c) { return base + (c == 0 ? p.part_rows : c * step); };
+    const float4 *values = reinterpret_cast<const float4 *>(p.part_o);
+    float4 v[kAhead];
+#pragma unroll
+    for (int c = 0; c < kAhead; ++c)
+        if (c < u.parts)
+            v[c] = values[row(c) * 16 + lane];
+    float2 ml = lane < u.parts ? p.part_ml[row(lane)] : make_float2(-INFINITY, 0.f);
+    float top = ml.x;
+    for (int c = lane + 16; c < u.parts; c += 16)
+        top = fmaxf(top, p.part_ml[row(c)].x);
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = 0; c0 < u.parts; c0 += 16) {
+        if (c0 > 0)
+            ml = c0 + lane < u.parts ? p.part_ml[row(c0 + lane)] : make_float2(-INFINITY, 0.f);
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
+        sum = fmaf(f, ml.y, sum);
+        const int n = min(16, u.parts - c0);
+        auto add = [&](float4 x, int c) {
+            const float w = __shfl_sync(0xffffffffu, f, c, 16);
+            o[0] = fmaf(w, x.x, o[0]);
+            o[1] = fmaf(w, x.y, o[1]);
+            o[2] = fmaf(w, x.z, o[2]);
+            o[3] = fmaf(w, x.w, o[3]);
         };
-        float top = -INFINITY, sum = 0.f, o0 = 0.f, o1 = 0.f;
-        // The first parts' values are on their way while the weights are found.
-        constexpr int kAhead = 12;
-        float2 v[kAhead];
+        int c = 0;
+        if (c0 == 0) {
 #pragma unroll
-        for (int c = 0; c < kAhead; ++c)
-            if (c < u.parts)
-                v[c] = reinterpret_cast<const float2 *>(p.part_o)[part(c) * 32 + lane];
-        constexpr int kSets = (kMaxCtas + 31) / 32;
-        float f[kSets], l[kSets];  // of parts lane, lane + 32, ...: the offset, then the weight; the sum
-#pragma unroll
-        for (int i = 0; i < kSets; ++i) {
-            const float2 ml = lane + 32 * i < u.parts ? p.part_ml[part(lane + 32 * i)] : make_float2(-INFINITY, 0.f);
-            f[i] = ml.x;
-            l[i] = ml.y;
-            top = fmaxf(top, ml.x);
+            for (; c < kAhead; ++c)
+                if (c < n)
+                    add(v[c], c);
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-#pragma unroll
-        for (int i = 0; i < kSets; ++i) {
-            f[i] = f[i] == -INFINITY ? 0.f : ex2_approx(f[i] - top);
-            sum = fmaf(f[i], l[i], sum);
-        }
-#pragma unroll
-        for (int c = 0; c < kAhead; ++c) {
-            const float w = __shfl_sync(0xffffffffu, f[0], c);
-            if (c < u.parts) {
-                o0 = fmaf(w, v[c].x, o0);
-                o1 = fmaf(w, v[c].y, o1);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kSets; ++i) {
 #pragma unroll 4
-            for (int c = max(kAhead, 32 * i); c < min(u.parts, 32 * i + 32); ++c) {
-                const float w = __shfl_sync(0xffffffffu, f[i], c & 31);
-                const float2 x = reinterpret_cast<const float2 *>(p.part_o)[part(c) * 32 + lane];
-                o0 = fmaf(w, x.x, o0);
-                o1 = fmaf(w, x.y, o1);
-            }
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int tok = p.by_group.div(r);
-        const int64_t id = static_cast<int64_t>(u.row0 + tok) * p.H + u.hk * p.group + r - tok * p.group;
-        reinterpret_cast<uint32_t *>(p.o + id * kHeadDim)[lane] = pack_bf16x2(o0 * inv, o1 * inv);
-        if (p.lse && lane == 0)
-            p.lse[id] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+        for (; c < n; ++c)
+            add(values[row(c0 + c) * 16 + lane], c);
     }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (!live)
+        return;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int tok = p.by_group.div(r);
+    const int64_t id = static_cast<int64_t>(u.row0 + tok) * p.H + u.hk * p.group + r - tok * p.group;
+    reinterpret_cast<uint2 *>(p.o + id * kHeadDim)[lane] =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    if (p.lse && lane == 0)
+        p.lse[id] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
 }
 
 } // namespace vggt

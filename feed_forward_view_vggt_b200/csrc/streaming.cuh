@@ -354,7 +354,9 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, vggt::cached_combine_kernel, p) != cudaSuccess)
+    if (cudaLaunchKernelEx(&cfg, p.part_rows <= vggt::kJoinRows ? vggt::cached_combine_kernel<12>
+                                                                : vggt::cached_combine_kernel<4>,
+                           p) != cudaSuccess)
         return VGGT_ERR_CUDA;
     return VGGT_OK;
 }
