@@ -14,33 +14,55 @@ namespace vggt {
 constexpr int kCacheMaxSeqs = 4096;
 constexpr int kPlanThreads = 256;
 
-struct PlanParams {
-    int n_seqs, page_size, n_pages, max_pages, n_rows, free_capacity;
-    const int32_t *cached, *fresh, *free_pages, *n_free;
-    int32_t *table, *cu_rows, *kv_lens, *slots, *counts;
+// x / d for 0 <= x < 2^31 by a multiplication (planning is a chain of
+// divisions with nothing else to do meanwhile): with
+// 2^(k-1) < d <= 2^k and mul = floor(2^(31+k) / d) + 1, mul d exceeds 2^(31+k)
+// by at most d <= 2^k, which moves the quotient of no x < 2^31.
+struct Divisor {
+    uint32_t d, mul, shift;
+
+    void set(uint32_t value)
+    {
+        d = value;
+        uint32_t k = 0;
+        while ((uint64_t{1} << k) < value)
+            ++k;
+        shift = k > 0 ? k - 1 : 0;
+        mul = k > 0 ? static_cast<uint32_t>((uint64_t{1} << (31 + k)) / value + 1) : 0;
+    }
+    __device__ __forceinline__ int div(int x) const
+    {
+        return d == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), mul) >> shift);
+    }
 };
 
-// Inclusive sums of a and b over the block's threads.
-__device__ __forceinline__ void block_scan2(int64_t &a, int64_t &b, int64_t (*part)[2])
+struct PlanParams {
+    int n_seqs, page_size, n_pages, max_pages, n_rows, free_capacity;
+    Divisor by_page;
+    const int32_t *cached, *fresh, *free_pages, *n_free;
+    int32_t *table, *cu_rows, *kv_lens, *slots, *counts;
+
+    // Pages of n positions.
+    __device__ __forceinline__ int pages(int n) const { return n > 0 ? by_page.div(n - 1) + 1 : 0; }
+};
+
+// Inclusive sums over the block's threads; `part` is used once.
+__device__ __forceinline__ int64_t block_scan(int64_t a, int64_t *part)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, a, d), y = __shfl_up_sync(0xffffffffu, b, d);
-        if (lane >= d) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, a, d);
+        if (lane >= d)
             a += x;
-            b += y;
-        }
     }
-    if (lane == 31) {
-        part[warp][0] = a;
-        part[warp][1] = b;
-    }
+    if (lane == 31)
+        part[warp] = a;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        a += part[w][0];
-        b += part[w][1];
-    }
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32 - 1; ++w)
+        a += w < warp ? part[w] : 0;
+    return a;
 }
 
 // The first index in [0, n) whose value is above x (n if none).
@@ -61,70 +83,69 @@ __device__ __forceinline__ int upper_bound(const int *v, int n, int x)
 // itself (a few loads each), so one launch does it all: the blocks share
 // nothing, and a row of a freshly taken page gets the page from the free
 // list and not from the block table that another block may be writing.
-// Bound by latency: the longest plan writes some hundred kilobytes.
+// Bound by latency: the longest plan writes some hundred kilobytes.  The
+// lengths are read once, into shared memory.
 __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanParams p)
 {
     extern __shared__ int plan_smem[];
     int *row_end = plan_smem;             // rows up to and with the sequence, at most n_rows
     int *need_end = row_end + p.n_seqs;   // pages taken up to and with the sequence
     int *state = need_end + p.n_seqs;     // pages held before the step, -1: refused
-    __shared__ int64_t part[kPlanThreads / 32][2];
-    __shared__ int refused;
+    int *held = state + p.n_seqs;         // positions before the step
+    __shared__ int64_t part[2][kPlanThreads / 32];
+    __shared__ int refused, taken_s;
     if (threadIdx.x == 0)
-        refused = 0;
+        refused = taken_s = 0;
     const int n_free = max(0, min(*p.n_free, p.free_capacity));
     const int per = (p.n_seqs + kPlanThreads - 1) / kPlanThreads;
     const int b0 = min(static_cast<int>(threadIdx.x) * per, p.n_seqs), b1 = min(b0 + per, p.n_seqs);
 
     // Rows first: whether a sequence's rows fit decides whether it asks for pages.
-    int64_t rows = 0, zero = 0;
-    for (int b = b0; b < b1; ++b)
-        rows += max(0, p.fresh[b]);
-    int64_t end = rows;
-    block_scan2(end, zero, part);
-    __syncthreads();
-    int64_t at = end - rows, need = 0;
+    int64_t rows = 0;
     for (int b = b0; b < b1; ++b) {
-        const int64_t c = max(0, p.cached[b]), n = max(0, p.fresh[b]);
+        const int n = max(0, p.fresh[b]);
+        held[b] = max(0, p.cached[b]);
+        need_end[b] = n;
+        rows += n;
+    }
+    int64_t at = block_scan(rows, part[0]) - rows, need = 0;
+    for (int b = b0; b < b1; ++b) {
+        const int c = held[b], n = need_end[b];
         at += n;
-        const int64_t have = (c + p.page_size - 1) / p.page_size, want = (c + n + p.page_size - 1) / p.page_size;
+        // past 2^31 - 1 positions the table is too small in any case
+        const int have = p.pages(c);
+        const int want = p.pages(static_cast<int>(min(static_cast<unsigned>(c) + static_cast<unsigned>(n), 0x7fffffffu)));
         const bool fits = at <= p.n_rows && want <= p.max_pages;
         row_end[b] = static_cast<int>(at < p.n_rows ? at : p.n_rows);
-        state[b] = fits ? static_cast<int>(have) : -1;
-        need += fits ? want - have : 0;
+        state[b] = fits ? have : -1;
+        need_end[b] = fits ? want - have : 0;
+        need += need_end[b];
+        if (blockIdx.x == 0)
+            p.kv_lens[b] = c + (fits && want == have ? n : 0);
     }
-    int64_t upto = need;
-    block_scan2(upto, zero, part);
-    upto -= need;
-    int missing = 0;
+    int64_t upto = block_scan(need, part[1]) - need;
+    int missing = 0, mine = 0;
     for (int b = b0; b < b1; ++b) {
-        const int c = max(0, p.cached[b]), n = max(0, p.fresh[b]);
-        int64_t take = 0;
-        if (state[b] >= 0)
-            take = (static_cast<int64_t>(c) + n + p.page_size - 1) / p.page_size - state[b];
-        const int64_t sum = upto + take;
-        if (state[b] >= 0 && take > 0 && sum > n_free)
+        const int take = need_end[b];
+        upto += take;
+        if (take > 0 && upto > n_free)
             state[b] = -1;
-        upto = sum;
+        else if (take > 0) {
+            mine = static_cast<int>(upto);
+            if (blockIdx.x == 0)
+                p.kv_lens[b] = held[b] + max(0, p.fresh[b]);
+        }
         // refused sequences come last among those that need pages, so their
         // sums stay at what was taken
-        need_end[b] = static_cast<int>(sum < n_free ? sum : n_free);
+        need_end[b] = static_cast<int>(upto < n_free ? upto : n_free);
         missing += state[b] < 0;
-        if (blockIdx.x == 0)
-            p.kv_lens[b] = state[b] < 0 ? c : c + n;
     }
     if (missing)
         atomicAdd(&refused, missing);
-    __syncthreads();
     // Pages taken: the sum of the last granted sequence that takes any.
     // (need_end of a refused one is cut at n_free, which is not what was taken.)
-    __shared__ int taken_s;
-    if (threadIdx.x == 0)
-        taken_s = 0;
-    __syncthreads();
-    for (int b = b0; b < b1; ++b)
-        if (state[b] >= 0 && need_end[b] > (b ? need_end[b - 1] : 0))
-            atomicMax(&taken_s, need_end[b]);
+    if (mine)
+        atomicMax(&taken_s, mine);
     __syncthreads();
     const int taken = taken_s;
     if (blockIdx.x == 0) {
@@ -146,12 +167,12 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
         const int b = upper_bound(row_end, p.n_seqs, static_cast<int>(r));
         int slot = -1;
         if (b < p.n_seqs && state[b] >= 0) {
-            const int pos = max(0, p.cached[b]) + static_cast<int>(r) - (b ? row_end[b - 1] : 0);
-            const int pi = pos / p.page_size;
+            const int pos = held[b] + static_cast<int>(r) - (b ? row_end[b - 1] : 0);
+            const int pi = p.by_page.div(pos);
             const int page = pi < state[b] ? p.table[static_cast<int64_t>(b) * p.max_pages + pi]
                                            : p.free_pages[n_free - 1 - ((b ? need_end[b - 1] : 0) + pi - state[b])];
             if (page >= 0 && page < p.n_pages)
-                slot = page * p.page_size + pos % p.page_size;
+                slot = page * p.page_size + pos - pi * p.page_size;
         }
         p.slots[r] = slot;
     }
@@ -160,6 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const PlanPara
 struct AppendParams {
     int n_rows, vecs;  // vecs: 16-byte vectors of a row, n_kv_heads * 8
     int page_size, n_slots;
+    Divisor by_vecs, by_page;
     int64_t row_stride, in_head_stride;              // new rows, in 16-byte vectors
     int64_t page_stride, head_stride, token_stride;  // pages, in 16-byte vectors
     const uint4 *k, *v;
@@ -168,26 +190,43 @@ struct AppendParams {
 };
 
 // K and V rows into their slots; a negative slot is skipped.  Bound by HBM:
-// every row of K and V is read once and written once.
+// every row of K and V is read once and written once (16 frames of 1374
+// tokens, 16 heads: 34 us as a graph, 5.3 TB/s).  A thread moves kEach vectors of K and of V, all
+// loads before the stores; small steps, which are bound by latency, spread over
+// more blocks with kEach = 1.
+template <int kEach>
 __global__ void __launch_bounds__(256) cache_append_kernel(const AppendParams p)
 {
-    const int64_t total = static_cast<int64_t>(p.n_rows) * p.vecs;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = i / p.vecs;
-        const int e = static_cast<int>(i - r * p.vecs), h = e >> 3, c = e & 7;
-        const int slot = p.slots[r];
+    const int64_t start = static_cast<int64_t>(blockIdx.x) * (256 * kEach), row0 = start / p.vecs;
+    const int in_row = static_cast<int>(start - row0 * p.vecs) + static_cast<int>(threadIdx.x);
+    uint4 k[kEach], v[kEach];
+    int64_t dst[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int at = in_row + 256 * i, below = p.by_vecs.div(at), e = at - below * p.vecs, h = e >> 3, c = e & 7;
+        const int64_t r = row0 + below;
+        dst[i] = -1;
+        if (r >= p.n_rows)
+            continue;
+        const int slot = __ldg(p.slots + r);
         if (slot < 0)
             continue;
         if (slot >= p.n_slots) {
             record_bounds_failure(kCheckCacheSlot);
             continue;
         }
-        const int page = slot / p.page_size, off = slot - page * p.page_size;
+        const int page = p.by_page.div(slot), off = slot - page * p.page_size;
+        dst[i] = page * p.page_stride + h * p.head_stride + off * p.token_stride + c;
         const int64_t src = r * p.row_stride + h * p.in_head_stride + c;
-        const int64_t dst = page * p.page_stride + h * p.head_stride + off * p.token_stride + c;
-        p.k_pages[dst] = p.k[src];
-        p.v_pages[dst] = p.v[src];
+        k[i] = p.k[src];
+        v[i] = p.v[src];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        if (dst[i] >= 0) {
+            p.k_pages[dst[i]] = k[i];
+            p.v_pages[dst[i]] = v[i];
+        }
     }
 }
 

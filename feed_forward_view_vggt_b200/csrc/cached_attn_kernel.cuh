@@ -66,28 +66,6 @@ constexpr int kSoftmaxWarps = 8;  // and with how many: 16 keys of a tile each
 enum : uint32_t { kSiteTaskFull = 12, kSiteTaskEmpty, kSiteMergeReady, kSiteMergeFree, kSiteFewQ, kSiteFewFull, kSiteTaskPassed };
 enum : int { kTaskSingle = 0, kTaskPair = 1, kTaskFew = 2 };
 
-// x / d for 0 <= x < 2^31 by a multiplication (the planning is a chain of
-// divisions, and nothing else runs while its first tasks are found): with
-// 2^(k-1) < d <= 2^k and mul = floor(2^(31+k) / d) + 1, mul d exceeds 2^(31+k)
-// by at most d <= 2^k, which moves the quotient of no x < 2^31.
-struct Divisor {
-    uint32_t d, mul, shift;
-
-    void set(uint32_t value)
-    {
-        d = value;
-        uint32_t k = 0;
-        while ((uint64_t{1} << k) < value)
-            ++k;
-        shift = k > 0 ? k - 1 : 0;
-        mul = k > 0 ? static_cast<uint32_t>((uint64_t{1} << (31 + k)) / value + 1) : 0;
-    }
-    __device__ __forceinline__ int div(int x) const
-    {
-        return d == 1 ? x : static_cast<int>(__umulhi(static_cast<uint32_t>(x), mul) >> shift);
-    }
-};
-
 // What a CTA leaves for the joining launch: the unit whose first part, but not
 // its last, was its work.  Parts 1, 2, ... are those of the CTAs behind it.
 struct Join {

@@ -57,7 +57,8 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8])
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Sum over the kWarps warps that share a row; every thread gets it.
+// Sum over the kWarps warps that share a row; every thread gets it.  `part`
+// is used once per row.
 template <int kWarps>
 __device__ __forceinline__ float row_sum(float v, float *part)
 {
@@ -66,7 +67,6 @@ __device__ __forceinline__ float row_sum(float v, float *part)
         v += __shfl_xor_sync(0xffffffffu, v, d);
     if (kWarps == 1)
         return v;
-    __syncthreads();
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = v;
     __syncthreads();
@@ -77,134 +77,122 @@ __device__ __forceinline__ float row_sum(float v, float *part)
     return t;
 }
 
-// t = N(t) over the row, kVec vectors of 8 channels per thread.  The
-// variance is taken about the mean in a second pass over registers: the
+// Factors (or terms) of the thread's channels c .. c + 7: read where they are
+// used, or kAhead, when the row's own values are.  None: `t` stays as it is.
+template <typename T, bool kAhead>
+struct Channels {
+    const T *p;
+    float v[8];
+
+    __device__ __forceinline__ Channels(const T *ptr, int c, bool in) : p(ptr ? ptr + c : nullptr)
+    {
+        if (kAhead && p && in)
+            load8(p, v);
+    }
+    __device__ __forceinline__ void scale(float (&t)[8])
+    {
+        if (p) {
+            if (!kAhead)
+                load8(p, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                t[e] *= v[e];
+        }
+    }
+    __device__ __forceinline__ void add(float (&t)[8])
+    {
+        if (p) {
+            if (!kAhead)
+                load8(p, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                t[e] += v[e];
+        }
+    }
+};
+
+// t = N(t) over the row; `in`: the thread has channels of it (else t is 0).
+// The variance is taken about the mean in a second pass over registers: the
 // values are there already, and E[t^2] - E[t]^2 would lose what a large
 // common offset leaves.
-template <int kVec, int kWarps>
-__device__ __forceinline__ void normalise(const NormParams &p, float (&t)[kVec][8], int lane, const float *w,
-                                          const float *b, float *part)
+template <int kWarps, bool kAhead>
+__device__ __forceinline__ void normalise(const NormParams &p, float (&t)[8], bool in, Channels<float, kAhead> &w,
+                                          Channels<float, kAhead> &b, float (*part)[kWarps])
 {
     float mean = 0.f;
     if (p.layer) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                s += t[i][e];
-        mean = row_sum<kWarps>(s, part) * p.inv_cols;
+        for (int e = 0; e < 8; ++e)
+            s += t[e];
+        mean = row_sum<kWarps>(s, part[0]) * p.inv_cols;
     }
     float q = 0.f;
+    if (in) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        if (8 * (lane + i * kWarps * 32) < p.n_cols) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                t[i][e] -= mean;
-                q = fmaf(t[i][e], t[i][e], q);
-            }
+        for (int e = 0; e < 8; ++e) {
+            t[e] -= mean;
+            q = fmaf(t[e], t[e], q);
         }
     }
-    const float r = rsqrtf(fmaf(row_sum<kWarps>(q, part), p.inv_cols, p.eps));
+    const float r = rsqrtf(fmaf(row_sum<kWarps>(q, part[1]), p.inv_cols, p.eps));
+    if (in) {
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const int c = 8 * (lane + i * kWarps * 32);
-        if (c < p.n_cols) {
-            float f[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                t[i][e] *= r;
-            if (w) {
-                load8(w + c, f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    t[i][e] *= f[e];
-            }
-            if (b) {
-                load8(b + c, f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    t[i][e] += f[e];
-            }
-        }
+        for (int e = 0; e < 8; ++e)
+            t[e] *= r;
+        w.scale(t);
+        b.add(t);
     }
 }
 
-// kWarps warps per row, the row in registers; one warp per row holds up to
-// 1024 channels.  Bound by HBM: x, y, x' and h once each.
-template <typename X, int kVec, int kWarps>
+// kWarps warps per row, 8 channels per thread, the row in registers.  Many
+// rows are bound by HBM (x, y, x' and h once each; 137400 x 1024, fp32 x: 264
+// us, 6.4 TB/s; with 32 channels per thread and a warp per row 266-268).  Few
+// rows (kAhead) are bound by the latency of a trip to memory and of the sums:
+// every load is issued at the start (17 x 1024: 6 us instead of 12).
+template <typename X, int kWarps, bool kAhead>
 __global__ void __launch_bounds__(kWarps > 4 ? 32 * kWarps : 128) norm_residual_kernel(const NormParams p)
 {
-    constexpr int kRows = kWarps > 4 ? 1 : 4 / kWarps;  // rows per block
-    __shared__ float part_s[kRows][kWarps];
-    const int lane = threadIdx.x % (32 * kWarps);
-    static_assert(kWarps == 1 || kRows == 1, "rows that share a block are one warp each");
-    float *part = part_s[threadIdx.x / (32 * kWarps)];
+    constexpr int kRows = kWarps == 1 ? 4 : 1;  // rows per block: those of one warp each share one
+    __shared__ float part_s[4][kWarps];
+    const int c = 8 * (threadIdx.x % (32 * kWarps));
     const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / (32 * kWarps);
     if (row >= p.n_rows)
         return;
-    const X *x = static_cast<const X *>(p.x) + row * p.x_stride;
-    float t[kVec][8];
+    const bool in = c < p.n_cols;
+    const X *x = static_cast<const X *>(p.x) + row * p.x_stride + c;
+    float t[8] = {}, xv[8];
+    if (p.y && in)
+        load8(p.y + row * p.y_stride + c, t);
+    if ((kAhead || !p.y) && in)
+        load8(x, xv);
+    Channels<float, kAhead> post_w(p.post_w, c, in), post_b(p.post_b, c, in), scale(p.scale, c, in);
+    Channels<__nv_bfloat16, kAhead> gate(p.gate ? p.gate + row / p.rows_per_gate * p.gate_stride : nullptr, c, in);
+    Channels<float, kAhead> w(p.w, c, in), b(p.b, c, in);
     if (p.y) {
-        const __nv_bfloat16 *y = p.y + row * p.y_stride;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int c = 8 * (lane + i * kWarps * 32);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                t[i][e] = 0.f;
-            if (c < p.n_cols)
-                load8(y + c, t[i]);
-        }
         if (p.post_norm)
-            normalise<kVec, kWarps>(p, t, lane, p.post_w, p.post_b, part);
-        const __nv_bfloat16 *gate = p.gate ? p.gate + row / p.rows_per_gate * p.gate_stride : nullptr;
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int c = 8 * (lane + i * kWarps * 32);
-            if (c < p.n_cols) {
-                float f[8];
-                if (p.scale) {
-                    load8(p.scale + c, f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        t[i][e] *= f[e];
-                }
-                if (gate) {
-                    load8(gate + c, f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        t[i][e] *= f[e];
-                }
-                load8(x + c, f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    t[i][e] += f[e];
-                if (p.x_out)
-                    store8(static_cast<X *>(p.x_out) + row * p.out_stride + c, t[i]);
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kVec; ++i) {
-            const int c = 8 * (lane + i * kWarps * 32);
+            normalise<kWarps, kAhead>(p, t, in, post_w, post_b, part_s);
+        if (in) {
+            if (!kAhead)
+                load8(x, xv);
+            scale.scale(t);
+            gate.scale(t);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                t[i][e] = 0.f;
-            if (c < p.n_cols)
-                load8(x + c, t[i]);
+                t[e] += xv[e];
+            if (p.x_out)
+                store8(static_cast<X *>(p.x_out) + row * p.out_stride + c, t);
         }
+    } else if (in) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            t[e] = xv[e];
     }
     if (!p.h)
         return;
-    normalise<kVec, kWarps>(p, t, lane, p.w, p.b, part);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) {
-        const int c = 8 * (lane + i * kWarps * 32);
-        if (c < p.n_cols)
-            store8(p.h + row * p.h_stride + c, t[i]);
-    }
+    normalise<kWarps, kAhead>(p, t, in, w, b, part_s + 2);
+    if (in)
+        store8(p.h + row * p.h_stride + c, t);
 }
 
 } // namespace vggt
