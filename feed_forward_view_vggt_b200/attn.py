@@ -560,89 +560,49 @@ def out_proj(o, w, shape, bias=None, stream=None):
 
 # ------------------------------------------------------- streaming (paged cache)
 #
-# A streaming step makes many small calls, so their cost on the host counts:
-# each tensor is looked at once (_use), the arguments go to the C entry point as
-# integers, and nothing is imported or looked up twice.
+# A streaming step makes many small calls, so their cost on the host counts: the
+# tensors are looked at, and what a call returns is allocated, in a compiled
+# module (csrc/streaming_binding.cpp); `stream` is that of the other calls.
 
-_T = None  # torch, once a call has needed it
+_host = None
+_entries = {}
+
+
+def _call(what, function, *args):
+    """`function` of the compiled module on the entry point `what` of the loaded library."""
+    global _host
+    if _host is None:
+        _torch()  # the module needs torch's libraries
+        try:
+            from . import _streaming
+        except ImportError as e:
+            raise RuntimeError("_streaming.so is not built; run `python -m feed_forward_view_vggt_b200.build`") from e
+        _host = _streaming
+    result = getattr(_host, function)(_entry(what), *args)
+    status = result if isinstance(result, int) else result[0]
+    if status != VGGT_OK:
+        raise VggtError(status, what)
+    return result
+
+
+def _entry(name):
+    """The address of an entry point of the loaded library."""
+    lib = load()
+    known = _entries.get(name)
+    if known is None or known[0] is not lib:
+        known = _entries[name] = (lib, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)
+    return known[1]
 
 
 def _torch():
-    global _T
-    if _T is None:
-        import torch
+    import torch
 
-        _T = torch
-    return _T
-
-
-def _use(x, dtype, device, name, contiguous=True):
-    """The address of a tensor of a call on CUDA device ``device`` (an index); None stays None."""
-    if x is None:
-        return None
-    if x.get_device() != device:
-        if not x.is_cuda:
-            raise ValueError(f"{name}: tensor must live on a CUDA device")
-        raise ValueError(f"{name}: tensor on cuda:{x.get_device()}, the call runs on cuda:{device}")
-    if x.dtype != dtype:
-        raise ValueError(f"{name}: expected dtype {dtype}, got {x.dtype}")
-    if contiguous and not x.is_contiguous():
-        raise ValueError(f"{name}: tensor must be contiguous")
-    return x.data_ptr()
-
-
-def _device(x, name):
-    """The index of the CUDA device of a call: that of its first tensor."""
-    device = x.get_device()
-    if device < 0:
-        raise ValueError(f"{name}: tensor must live on a CUDA device")
-    return device
-
-
-def _launch(status_of, device, args, stream, what):
-    """Calls an entry point on its device and on `stream` (None: torch's current stream of that device)."""
-    torch = _torch()
-    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    if torch.cuda.current_device() == device:
-        status = status_of(*args, raw)
-    else:
-        with torch.cuda.device(device):
-            status = status_of(*args, raw)
-    if status != VGGT_OK:
-        raise VggtError(status, what)
-
-
-def _new(shape, dtype, device, stream, returned=True):
-    """A buffer of a call on `stream`: allocated there, since memory that was freed on torch's current stream may still
-    be in use on it, and (if it is returned) freed only after the work of the current stream that reads it."""
-    torch = _torch()
-    device = torch.device("cuda", device)
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream):
-        x = torch.empty(shape, dtype=dtype, device=device)
-    if returned:
-        x.record_stream(torch.cuda.current_stream(device))
-    return x
+    return torch
 
 
 def _expect(ok, what):
     if not ok:
         raise ValueError(what)
-
-
-def _page_layout(k_pages, v_pages, n_heads, n_seqs, max_pages):
-    shape, stride = k_pages.shape, k_pages.stride()
-    _expect(len(shape) == 4 and shape == v_pages.shape and stride == v_pages.stride() and
-            (stride[3] == 1 or shape[3] == 1),
-            "k_pages, v_pages: [n_pages, n_kv_heads, page_size, head_dim] of the same strides, the last one 1")
-    n_pages, n_kv_heads, page_size, head_dim = shape
-    sp, sh, st, _ = stride
-    if n_pages == 1:  # a single page or head has no stride
-        sp = 64
-    if n_kv_heads == 1:
-        sh = 64
-    return vggt_cache(n_seqs, n_heads, n_kv_heads, head_dim, page_size, n_pages, max_pages, sp, sh, st)
 
 
 def cache_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size, n_rows, n_pages=None, stream=None):
@@ -651,53 +611,16 @@ def cache_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size
     [free pages left, sequences refused] and counts[:1] the next step's n_free.
     n_rows: rows of the step's packed buffers (>= the new rows).  n_pages: pages
     of the cache (default: as many as 32-bit slots allow)."""
-    torch = _torch()
-    _expect(block_table.dim() == 2 and cached_lens.numel() == new_lens.numel() == block_table.shape[0]
-            and n_free.numel() == 1, "one cached length, new length and row of block_table per sequence, one n_free")
-    seqs, max_pages = block_table.shape
     if n_pages is None:
         n_pages = (2 ** 31 - 1) // page_size if page_size > 0 else 1
-    d, i32 = _device(block_table, "block_table"), torch.int32
-    inputs = (_use(cached_lens, i32, d, "cached_lens"), _use(new_lens, i32, d, "new_lens"),
-              _use(free_pages, i32, d, "free_pages"), free_pages.numel(), _use(n_free, i32, d, "n_free"),
-              _use(block_table, i32, d, "block_table"), n_rows)
-    # one buffer: every part starts on 4 bytes, which is all that is asked
-    out = _new(2 * seqs + 3 + max(n_rows, 0), i32, d, stream)
-    at = out.data_ptr()
-    cu, kv = at + 8, at + 12 + 4 * seqs
-    slots = kv + 4 * seqs
-    _launch(load().vggt_cache_plan, d, (vggt_cache(seqs, 1, 1, 64, page_size, n_pages, max_pages, 64, 64, 64), *inputs,
-                                        cu, kv, slots, at), stream, "vggt_cache_plan")
-    counts, cu_rows, kv_lens, slots = torch.split_with_sizes(out, (2, seqs + 1, seqs, n_rows))
-    return cu_rows, kv_lens, slots, counts
+    return _call("vggt_cache_plan", "plan", cached_lens, new_lens, free_pages, n_free, block_table, page_size, n_rows,
+                 n_pages, stream)[1:]
 
 
 def cache_append(k, v, slots, k_pages, v_pages, stream=None):
     """Writes the rows of k and v ([n_rows, n_kv_heads, 64], rows and heads may
     be strided) into their slots of k_pages and v_pages."""
-    shape = k.shape
-    _expect(len(shape) == 3 and shape == v.shape and k.stride() == v.stride() and slots.shape == shape[:1],
-            "k, v: [n_rows, n_kv_heads, head_dim] of the same strides, one slot per row")
-    cache = _page_layout(k_pages, v_pages, shape[1], 1, 1)
-    _expect(shape[1] == cache.n_kv_heads and shape[2] == cache.head_dim, "k, v: the heads and head_dim of the pages")
-    d, bf16 = _device(k_pages, "k_pages"), _torch().bfloat16
-    row, head = _row_strides(k)
-    _launch(load().vggt_cache_append, d,
-            (cache, _use(k, bf16, d, "k", False), _use(v, bf16, d, "v", False), row, head,
-             _use(slots, _T.int32, d, "slots"), shape[0], _use(k_pages, bf16, d, "k_pages", False),
-             _use(v_pages, bf16, d, "v_pages", False)), stream, "vggt_cache_append")
-
-
-def _row_strides(x):
-    row, head, last = x.stride()
-    rows, heads, dim = x.shape
-    _expect(last == 1 or dim == 1, "the last dimension must be contiguous")
-    # a dimension of one element has no stride of its own: any valid one does
-    if heads <= 1:
-        head = 64
-    if rows <= 1:
-        row = max(64, head * heads)
-    return row, head
+    _call("vggt_cache_append", "append", k, v, slots, k_pages, v_pages, stream)
 
 
 def cached(q, k_pages, v_pages, block_table, cu_rows, kv_lens, causal_unit=0, scale=None, want_lse=False,
@@ -705,34 +628,9 @@ def cached(q, k_pages, v_pages, block_table, cu_rows, kv_lens, causal_unit=0, sc
     """Attention of the new rows q ([n_rows, H, 64], rows and heads may be
     strided) over a paged cache; see vggt_attn_cached for the mask.  Rows
     behind cu_rows[-1] keep what ``o`` holds (uninitialised if not given)."""
-    torch = _torch()
-    shape, tables = q.shape, block_table.shape
-    _expect(len(shape) == 3 and shape[2] == k_pages.shape[-1], "q: [n_rows, n_heads, head_dim]")
-    _expect(len(tables) == 2 and kv_lens.numel() == tables[0] == cu_rows.numel() - 1,
-            "one row of block_table and one length per sequence, one row offset more")
-    _expect(o is None or o.shape == shape, "o: the shape of q")
-    rows, heads, _ = shape
-    cache = _page_layout(k_pages, v_pages, heads, *tables)
-    d, bf16, i32 = _device(q, "q"), torch.bfloat16, torch.int32
-    row, head = _row_strides(q)
-    inputs = (cache, _use(q, bf16, d, "q", False), row, head, _use(k_pages, bf16, d, "k_pages", False),
-              _use(v_pages, bf16, d, "v_pages", False), _use(block_table, i32, d, "block_table"),
-              _use(cu_rows, i32, d, "cu_rows"), _use(kv_lens, i32, d, "kv_lens"), rows, causal_unit)
-    lib, lse = load(), None
-    if o is None:
-        o = _new(shape, bf16, d, stream)
-    if want_lse:
-        lse = _new((rows, heads), torch.float32, d, stream)
-    if workspace is None:
-        nbytes = lib.vggt_attn_cached_workspace_bytes(cache, rows)
-        if nbytes:
-            workspace = _new(nbytes, torch.uint8, d, stream, returned=False)
-    else:
-        nbytes = workspace.numel() * workspace.element_size()
-    _launch(lib.vggt_attn_cached, d,
-            (*inputs, _use(o, bf16, d, "o"), None if lse is None else lse.data_ptr(),
-             None if workspace is None else _use(workspace, workspace.dtype, d, "workspace"), nbytes,
-             default_scale(shape[2]) if scale is None else scale), stream, "vggt_attn_cached")
+    _, o, lse = _call("vggt_attn_cached", "attend", _entry("vggt_attn_cached_workspace_bytes"), q, k_pages, v_pages,
+                      block_table, cu_rows, kv_lens, causal_unit,
+                      default_scale(q.shape[-1]) if scale is None else scale, want_lse, workspace, o, stream)
     return (o, lse) if want_lse else o
 
 
@@ -741,44 +639,9 @@ def norm_residual(x, y=None, kind="layer", eps=1e-6, scale=None, gate=None, rows
     """x' = x + scale * gate * N_post(y) and h = N_pre(x') in one pass over the
     rows of x and y ([n_rows, n_cols]); returns (x', h).  Without y x' is x;
     with want_h false h is None; with inplace x' overwrites x."""
-    torch = _torch()
-    shape = x.shape
-    _expect(len(shape) == 2 and (y is None or y.shape == shape), "x, y: [n_rows, n_cols]")
     _expect(kind in _NORM_KINDS, "kind: 'layer' or 'rms'")
-    rows, cols = shape
-    if gate is None:
-        rows_per_gate = 0
-    else:
-        _expect(rows_per_gate >= 1 and gate.shape == (-(-rows // rows_per_gate), cols),
-                "gate: [ceil(n_rows / rows_per_gate), n_cols]")
-    xt, f32, bf16 = x.dtype, torch.float32, torch.bfloat16
-    _expect(xt == f32 or xt == bf16, "x: float32 or bfloat16")
-    d = _device(x, "x")
-
-    def factors(t, name):
-        _expect(t is None or t.shape == (cols,), f"{name}: [n_cols]")
-        return _use(t, f32, d, name)
-
-    def stride(t, name):
-        if t is None:
-            return cols
-        row, col = t.stride()
-        _expect(col == 1 or cols == 1, f"{name}: the last dimension must be contiguous")
-        return row if rows > 1 else cols
-
-    inputs = (_use(x, xt, d, "x", False), _use(y, bf16, d, "y", False), factors(post_weight, "post_weight"),
-              factors(post_bias, "post_bias"), factors(scale, "scale"), _use(gate, bf16, d, "gate"),
-              factors(weight, "weight"), factors(bias, "bias"))
-    xs, ys = stride(x, "x"), stride(y, "y")
-    out = None
-    if y is not None:
-        out = x if inplace else _new(shape, xt, d, stream)
-    h = _new(shape, bf16, d, stream) if want_h else None
-    norm = vggt_norm(rows, cols, _NORM_KINDS[kind], xt == f32, bool(post_norm), rows_per_gate, eps, xs, ys,
-                     xs if inplace else cols, cols)
-    _launch(load().vggt_norm_residual, d, (norm, *inputs, None if out is None else out.data_ptr(),
-                                           None if h is None else h.data_ptr()), stream, "vggt_norm_residual")
-    return (x if out is None else out), h
+    return _call("vggt_norm_residual", "norm", x, y, _NORM_KINDS[kind], eps, scale, gate, rows_per_gate, post_norm,
+                 post_weight, post_bias, weight, bias, want_h, inplace, stream)[1:]
 
 
 class PagedCache:

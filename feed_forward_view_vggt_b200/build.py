@@ -1,4 +1,5 @@
-"""Builds libvggt_attn.so in-tree with nvcc for sm_100a.
+"""Builds libvggt_attn.so in-tree with nvcc for sm_100a, and _streaming.so, the
+torch side of the streaming calls, with g++.
 
     python -m feed_forward_view_vggt_b200.build [--verbose] [--debug]
 
@@ -26,6 +27,10 @@ SOURCES = [os.path.join(CSRC, "vggt_attn.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + \
     [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
 
+# torch-side marshalling of the streaming calls (a Python extension module)
+BINDING = os.path.join(HERE, "_streaming.so")
+BINDING_SOURCE = os.path.join(CSRC, "streaming_binding.cpp")
+
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
@@ -51,6 +56,7 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     """Builds the release library, or with debug=True the library with
     device index checks (-DVGGT_DEBUG); returns its path."""
     lib = DEBUG_LIB if debug else LIB
+    build_binding(force=force and not debug, verbose=verbose)
     if not force and up_to_date(lib):
         return lib
     tmp = lib + ".tmp.%d" % os.getpid()
@@ -62,6 +68,32 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
     subprocess.run(cmd, check=True)
     os.replace(tmp, lib)
     return lib
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Builds the torch-side module of the streaming calls; returns its path."""
+    deps = [BINDING_SOURCE] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(BINDING) >= os.path.getmtime(p) for p in deps):
+        return BINDING
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) if os.path.isabs(nvcc()) else "/usr/local/cuda"
+    tmp = BINDING + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           "-o", tmp, BINDING_SOURCE, "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

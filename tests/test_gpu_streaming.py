@@ -265,7 +265,7 @@ def test_attention_is_repeatable_and_runs_on_two_streams_at_once():
 def test_attention_replays_with_the_lengths_of_the_replay():
     b = ref.Batch([2000, 500], [1, 1], 16, 8, 2, seed=31)
     o, ws = torch.empty_like(b.q), None
-    cache = attn._page_layout(b.k_pages, b.v_pages, 8, *b.table.shape)
+    cache = attn.vggt_cache(2, 8, 2, D, 16, b.k_pages.shape[0], b.table.shape[1], *b.k_pages.stride()[:3])
     ws = torch.empty(max(256, attn.vggt_attn_cached_workspace_bytes(cache, 2)), dtype=torch.uint8, device="cuda")
     call = lambda: attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, causal_unit=1, o=o,  # noqa: E731
                                workspace=ws)
