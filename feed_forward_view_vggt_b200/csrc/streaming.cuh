@@ -342,21 +342,26 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
         return VGGT_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const unsigned grid = static_cast<unsigned>(num_sms < vggt::kMaxCtas ? num_sms : vggt::kMaxCtas);
-    vggt::cached_attn_kernel<<<grid, vggt::kAttnThreads, vggt::cached_smem_bytes(cache.n_seqs), s>>>(tq, tk, tv, p);
-    if ((st = launched()) != VGGT_OK || need == 0)
-        return st;
-    // The joining launch is set up while the attention runs and waits for its
+    // Both launches are set up while the one before them runs and wait for its
     // end on the device.
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
-    cfg.gridDim = dim3(grid, static_cast<unsigned>((p.part_rows + vggt::kJoinRows - 1) / vggt::kJoinRows));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(vggt::kAttnThreads);
+    cfg.dynamicSmemBytes = vggt::cached_smem_bytes(cache.n_seqs);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, vggt::cached_attn_kernel, tq, tk, tv, p) != cudaSuccess)
+        return VGGT_ERR_CUDA;
+    if (need == 0)
+        return VGGT_OK;
+    cfg.gridDim = dim3(grid, static_cast<unsigned>((p.part_rows + vggt::kJoinRows - 1) / vggt::kJoinRows));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     if (cudaLaunchKernelEx(&cfg, p.part_rows <= vggt::kJoinRows ? vggt::cached_combine_kernel<12>
                                                                 : vggt::cached_combine_kernel<4>,
                            p) != cudaSuccess)
