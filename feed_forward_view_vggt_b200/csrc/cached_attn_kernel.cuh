@@ -194,18 +194,24 @@ __device__ __forceinline__ int tiles_before(const CachedParams &p, const Unit &u
 }
 
 // Sums the costs: work_end and work.  Every thread takes a run of consecutive
-// sequences; one with many pairs of unequal length is summed by its warp.
+// sequences; one with many pairs of unequal length is summed by its warp.  The
+// host chose cost_shift for row offsets that ascend and stay below n_rows; with
+// others there is no work, and the error word says so.
 __device__ __forceinline__ void plan_work(CachedSmem &sm, const CachedParams &p)
 {
     constexpr int kLong = 8;
     const int tid = threadIdx.x, lane = tid & 31;
     const int per = (p.n_seqs + kAttnThreads - 1) / kAttnThreads;
     int mine = 0;
+    bool bad = false;
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
         Seq s{0, 0, 0};
-        if (b < p.n_seqs)
+        if (b < p.n_seqs) {
             s = load_seq(p, b);
+            const int row0 = __ldg(p.cu_rows + b), row1 = __ldg(p.cu_rows + b + 1);
+            bad = bad || row0 < 0 || row1 < row0 || row1 > p.n_rows;
+        }
         const int units = unit_count(p, s);
         int sum = 0;
         bool loop = false;
@@ -247,14 +253,17 @@ __device__ __forceinline__ void plan_work(CachedSmem &sm, const CachedParams &p)
     }
     if (lane == 31)
         sm.scan[tid >> 5] = upto;
-    __syncthreads();
+    bad = __syncthreads_or(bad);
     for (int w = 0; w < (tid >> 5); ++w)
         upto += sm.scan[w];
     if (upto != mine)
         for (int b = tid * per; b < min((tid + 1) * per, p.n_seqs); ++b)
             sm.work_end[b] += upto - mine;
-    if (tid == kAttnThreads - 1)
-        sm.work = upto;
+    if (tid == kAttnThreads - 1) {
+        sm.work = bad ? 0 : upto;
+        if (bad)
+            record_bounds_failure(kCheckCacheRows);
+    }
 }
 
 // --------------------------------------------------------------- roles
@@ -1256,8 +1265,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     CachedSmem &sm = *reinterpret_cast<CachedSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                      ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // The joining launch may be set up; it waits for this one before it reads.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.q_full[i]), 1);
@@ -1311,6 +1318,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
+    // The joining launch may be set up; it waits for this one before it reads.
+    // (Not before the TMEM allocation: what comes early may want TMEM too.)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // 168 registers/thread at launch; 128 x (72 + 216 + 216) = 384 x 168.
     if (warp < 4) {

@@ -4,8 +4,8 @@
 // Bits of g_vggt_error:
 //   bit 0        a bounded wait ran out (kErrTimeout); bits 8..15 = the code
 //                of the first wait site that gave up;
-//   bit 1        an index check failed (kErrBounds): a slot or page of the
-//                caller's own in any build, a computed index in one built
+//   bit 1        an index check failed (kErrBounds): a slot, page or row
+//                offset of the caller's own in any build, a computed index in one built
 //                with -DVGGT_DEBUG; bits 16..23 = the code of the first
 //                check site that failed.
 // vggt_check() reads and clears the word.
@@ -25,7 +25,8 @@ enum : uint32_t {
     kCheckIndexToken,    // index build: kept token id
     kCheckQkvRow,        // QKV projection epilogue: output row
     kCheckCacheSlot,     // cache append: a slot of the slot map (every build)
-    kCheckCachePage      // cached attention: a page of the block table (every build)
+    kCheckCachePage,     // cached attention: a page of the block table (every build)
+    kCheckCacheRows      // cached attention: row offsets that do not ascend (every build)
 };
 
 __device__ unsigned int g_vggt_error;

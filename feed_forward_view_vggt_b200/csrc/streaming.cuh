@@ -355,18 +355,15 @@ VGGT_API vggt_status vggt_attn_cached(vggt_cache cache, const void *q, int64_t q
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, vggt::cached_attn_kernel, tq, tk, tv, p) != cudaSuccess)
-        return VGGT_ERR_CUDA;
-    if (need == 0)
-        return VGGT_OK;
+    cudaLaunchKernelEx(&cfg, vggt::cached_attn_kernel, tq, tk, tv, p);
+    if ((st = launched()) != VGGT_OK || need == 0)
+        return st;
     cfg.gridDim = dim3(grid, static_cast<unsigned>((p.part_rows + vggt::kJoinRows - 1) / vggt::kJoinRows));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    if (cudaLaunchKernelEx(&cfg, p.part_rows <= vggt::kJoinRows ? vggt::cached_combine_kernel<12>
-                                                                : vggt::cached_combine_kernel<4>,
-                           p) != cudaSuccess)
-        return VGGT_ERR_CUDA;
-    return VGGT_OK;
+    cudaLaunchKernelEx(
+        &cfg, p.part_rows <= vggt::kJoinRows ? vggt::cached_combine_kernel<12> : vggt::cached_combine_kernel<4>, p);
+    return launched();
 }
 
 namespace {
@@ -421,6 +418,8 @@ VGGT_API vggt_status vggt_norm_residual(vggt_norm norm, const void *x, const voi
         return VGGT_ERR_INVALID_ARG;
     if (norm.n_cols % 8 != 0 || norm.n_cols > vggt::kNormMaxCols || norm.n_rows > INT32_MAX - 1024)
         return VGGT_ERR_UNSUPPORTED;
+    if (norm.n_rows == 0)
+        return VGGT_OK;
     if (!y && (post_w || post_b || scale || gate || x_out || norm.post_norm))
         return VGGT_ERR_INVALID_ARG;
     if ((!norm.post_norm && (post_w || post_b)) || (!h && (w || b)) || (!x_out && !h))
@@ -431,8 +430,6 @@ VGGT_API vggt_status vggt_norm_residual(vggt_norm norm, const void *x, const voi
     if (!stride_ok(norm.x_stride, C) || (y && !stride_ok(norm.y_stride, C)) ||
         (x_out && !stride_ok(norm.out_stride, C)) || (h && !stride_ok(norm.h_stride, C)))
         return VGGT_ERR_INVALID_ARG;
-    if (R == 0)
-        return VGGT_OK;
     if (!x)
         return VGGT_ERR_INVALID_ARG;
     const size_t xw = norm.x_fp32 ? 4 : 2;

@@ -427,7 +427,8 @@ vggt_status vggt_cache_append(vggt_cache cache, const void *k, const void *v, in
  * ceil(kv_lens / page_size) entries of a row are read; a page outside
  * [0, n_pages) is not read and reported by vggt_check (VGGT_ERR_BOUNDS), the
  * rows of its sequence are then unspecified.  cu_rows: int32 [n_seqs + 1],
- * ascending from 0, at most n_rows.  kv_lens: int32 [n_seqs], cut at 0 and
+ * ascending, in [0, n_rows]; otherwise nothing is computed and vggt_check
+ * reports it (VGGT_ERR_BOUNDS).  kv_lens: int32 [n_seqs], cut at 0 and
  * max_pages * page_size.  workspace: device, 256-byte aligned,
  * vggt_attn_cached_workspace_bytes() bytes (0: may be NULL), overwritten;
  * calls that may run at the same time need one each.  The lengths are read

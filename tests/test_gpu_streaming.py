@@ -247,6 +247,81 @@ def test_attention_skips_and_reports_a_page_outside_the_cache():
     ok()
 
 
+@pytest.mark.parametrize("cu", [[0, 5, 3, 9], [-1, 3, 4, 9], [0, 3, 4, 10], [0, 9, 0, 9]])
+def test_attention_refuses_row_offsets_that_do_not_ascend(cu):
+    b = ref.Batch([400, 300, 20], [3, 4, 2], 16, 2, 2, seed=2)
+    o = torch.full_like(b.q, 5.0)
+    attn.cached(b.q, b.k_pages, b.v_pages, b.table, i32(cu), b.kv_lens, o=o)
+    assert attn.vggt_check()[0] == attn.VGGT_ERR_BOUNDS
+    assert (o == 5.0).all()
+    got = attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, o=o)
+    ok()
+    check_attention(b, 0, got)
+
+
+def test_calls_without_rows():
+    b = ref.Batch([40, 0], [0, 0], 16, 4, 2, seed=2)
+    got, lse = attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, want_lse=True)
+    assert got.shape == (0, 4, D) and lse.shape == (0, 4)
+    attn.cache_append(b.q[:, :2], b.q[:, :2], i32([]), b.k_pages, b.v_pages)
+    x, h = attn.norm_residual(torch.zeros(0, 64, device="cuda"), torch.zeros(0, 64, device="cuda").bfloat16())
+    assert x.shape == h.shape == (0, 64)
+    # rows of the buffer, none of a sequence
+    o = torch.full((7, 4, D), 3.0, device="cuda").bfloat16()
+    attn.cached(o.clone(), b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, o=o)
+    ok()
+    assert (o == 3.0).all()
+
+
+def test_calls_on_another_stream_than_the_current_one():
+    """Inputs made on the current stream, a call on another one that waits for it, results read on the current one:
+    twice at once, so that the buffers of both calls are in flight together."""
+    side = torch.cuda.Stream()
+    b = ref.Batch([700, 300, 41], [1, 150, 2], 16, 8, 2, seed=4)
+    x = torch.randn(500, 256, device="cuda")
+    y = torch.randn(500, 256, device="cuda").bfloat16()
+    want_x, want_h = attn.norm_residual(x, y)
+    want_o = attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, causal_unit=1)
+    table = b.table.clone()
+    plan_args = (i32([700, 300, 41]), i32([1, 150, 2]), i32(list(range(30))), i32([30]))
+    want_plan = attn.cache_plan(*plan_args, table.clone(), 16, 160)
+    for _ in range(5):
+        side.wait_stream(torch.cuda.current_stream())
+        got = attn.norm_residual(x, y, stream=side)
+        raw = attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, causal_unit=1,
+                          stream=side.cuda_stream)
+        scratch = [torch.full((500, 256), float("nan"), device="cuda") for _ in range(8)]
+        plan = attn.cache_plan(*plan_args, table.clone(), 16, 160, stream=side)
+        del scratch
+        torch.cuda.current_stream().wait_stream(side)
+        assert torch.equal(got[0], want_x) and torch.equal(got[1], want_h) and torch.equal(raw, want_o)
+        assert all(torch.equal(p, q) for p, q in zip(plan, want_plan))
+    ok()
+
+
+def test_norm_and_append_replay():
+    x, y = torch.randn(40, 768, device="cuda"), torch.randn(40, 768, device="cuda").bfloat16()
+    b = ref.Batch([64], [0], 16, 2, 2)
+    k, slots = torch.randn(4, 2, D, device="cuda").bfloat16(), i32([3, 60, -1, 17])
+    graph = torch.cuda.CUDAGraph()
+    attn.norm_residual(x, y)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got_x, got_h = attn.norm_residual(x, y)
+        attn.cache_append(k, k, slots, b.k_pages, b.v_pages)
+    for seed in (1, 2):
+        torch.manual_seed(seed)
+        x.normal_()
+        y.copy_(torch.randn(40, 768))
+        k.copy_(torch.randn(4, 2, D))
+        graph.replay()
+        want_x, want_h = attn.norm_residual(x, y)
+        assert torch.equal(got_x, want_x) and torch.equal(got_h, want_h)
+        for r, s in ((0, 3), (1, 60), (3, 17)):
+            assert torch.equal(b.k_pages[s // 16, :, s % 16], k[r]) and torch.equal(b.v_pages[s // 16, :, s % 16], k[r])
+    ok()
+
+
 def test_attention_is_repeatable_and_runs_on_two_streams_at_once():
     a = ref.Batch([9000, 41, 700], [1, 1, 1], 16, 16, 4, seed=21)
     c = ref.Batch([1374 * 3], [1374], 128, 4, 4, seed=22)
