@@ -29,9 +29,18 @@
 // CTA (384 threads, one per SM): warps 0 and 3 load Q and K, and V, by TMA, page
 // by page (a 4-D map of the pages; a box is the largest power of two of rows
 // that divides the page, at most 128); warp 0 also walks along the CTA's work
-// and writes its tasks into a ring; warps 1 and 2 issue the UMMAs; warps 4-7 and 8-11 are the softmax warpgroups.
-// TMEM, score buffers and the order S(k+3) after PV(k) are those of
-// attn_fwd_kernel.
+// and writes its tasks into a ring; warps 1 and 2 issue the UMMAs; warps 4-7
+// and 8-11 are the softmax warpgroups.  TMEM, score buffers and the order S(k+3)
+// after PV(k) are those of attn_fwd_kernel.
+//
+// Bound by the exponentials and the instructions around them, as that kernel
+// is: one frame of 1374 tokens over 100 cached ones, 16 heads, 0.94 ms or 830
+// TFLOP/s alone, 1.07 ms or 730 in a row under the power cap.  Single tokens are
+// bound by HBM: 148 sequences of 32000 keys 6.9 TB/s, 48 of odd lengths in pages
+// of 16, with grouped heads, 178 us or 4.8 TB/s.  Small calls are bound by
+// latency: planning 0.8 us, finding the first task 1.2 us, first keys 1.5 us,
+// the end of a task 1.5 us, the joining launch 2 us (one token over 5496 keys
+// and 16 heads: 12 us in a graph).
 //
 // Keys behind kv are never used, whatever the page holds there: their scores
 // are masked, their V rows are zeroed in shared memory up to the next multiple
@@ -57,8 +66,11 @@ constexpr int kMaxCtas = 148;
 constexpr int kCachedPolyPairs = 3;
 constexpr int kTaskRing = 8;
 // What a unit costs beside its steps (Q load, first score, epilogue), in
-// steps, and the fewest steps a CTA is used for.
-constexpr int kUnitCost = 6, kFewUnitCost = 1, kMinSteps = 4;
+// steps, and the fewest steps a CTA is used for.  Measured over fourteen small
+// and middle calls, geometric mean: (1, 4) for the last two 20.3 us, (3, 4)
+// 19.1, (3, 3) 18.8, (3, 2) 18.9, (1, 1) 19.5, (6, 4) 19.1; 3, 10 and 16 for the
+// first within 0.3% of 6.
+constexpr int kUnitCost = 6, kFewUnitCost = 3, kMinSteps = 3;
 
 constexpr int kFewRows = 16;      // rows of a task that the warps work on by themselves
 constexpr int kSoftmaxWarps = 8;  // and with how many: 16 keys of a tile each
