@@ -57,8 +57,8 @@ __device__ __forceinline__ void store8(float *p, const float (&v)[8])
     reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// Sum over the kWarps warps that share a row; every thread gets it.  `part`
-// is used once per row.
+// Sum over the warps that share a row, at most kWarps: the block's if there is
+// more than one.  Every thread gets it.  `part` is used once per row.
 template <int kWarps>
 __device__ __forceinline__ float row_sum(float v, float *part)
 {
@@ -70,10 +70,11 @@ __device__ __forceinline__ float row_sum(float v, float *part)
     if ((threadIdx.x & 31) == 0)
         part[threadIdx.x >> 5] = v;
     __syncthreads();
+    const int warps = static_cast<int>(blockDim.x >> 5);
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i)
-        t += part[i];
+        t += i < warps ? part[i] : 0.f;
     return t;
 }
 
@@ -145,7 +146,8 @@ __device__ __forceinline__ void normalise(const NormParams &p, float (&t)[8], bo
     }
 }
 
-// kWarps warps per row, 8 channels per thread, the row in registers.  Many
+// One warp per 256 channels of a row, 8 channels per thread, the row in
+// registers; kWarps = 1: four rows per block, else the block is a row's.  Many
 // rows are bound by HBM (x, y, x' and h once each; 137400 x 1024, fp32 x: 264
 // us, 6.4 TB/s; with 32 channels per thread and a warp per row 266-268).  Few
 // rows (kAhead) are bound by the latency of a trip to memory and of the sums:
@@ -155,8 +157,8 @@ __global__ void __launch_bounds__(kWarps > 4 ? 32 * kWarps : 128) norm_residual_
 {
     constexpr int kRows = kWarps == 1 ? 4 : 1;  // rows per block: those of one warp each share one
     __shared__ float part_s[4][kWarps];
-    const int c = 8 * (threadIdx.x % (32 * kWarps));
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / (32 * kWarps);
+    const int c = 8 * (kWarps == 1 ? threadIdx.x & 31 : threadIdx.x);
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (kWarps == 1 ? threadIdx.x >> 5 : 0);
     if (row >= p.n_rows)
         return;
     const bool in = c < p.n_cols;

@@ -372,8 +372,9 @@ template <typename X, int kWarps, bool kAhead>
 void launch_norm(const vggt::NormParams &p, cudaStream_t s)
 {
     constexpr int rows = kWarps == 1 ? 4 : 1;
+    const unsigned threads = kWarps == 1 ? 128 : 32 * ((static_cast<unsigned>(p.n_cols) + 255) / 256);
     vggt::norm_residual_kernel<X, kWarps, kAhead>
-        <<<static_cast<unsigned>((p.n_rows + rows - 1) / rows), 32 * kWarps * rows, 0, s>>>(p);
+        <<<static_cast<unsigned>((p.n_rows + rows - 1) / rows), threads, 0, s>>>(p);
 }
 
 // Measured both sides: 128 rows, 8.2 us ahead against 8.2-10.2 (256 to 4096
@@ -394,8 +395,6 @@ void launch_norm_cols(const vggt::NormParams &p, cudaStream_t s)
 {
     if (p.n_cols <= 256)
         launch_norm_rows<X, 1>(p, s);
-    else if (p.n_cols <= 512)
-        launch_norm_rows<X, 2>(p, s);
     else if (p.n_cols <= 1024)
         launch_norm_rows<X, 4>(p, s);
     else if (p.n_cols <= 2048)
