@@ -259,6 +259,42 @@ def test_attention_refuses_row_offsets_that_do_not_ascend(cu):
     check_attention(b, 0, got)
 
 
+def test_attention_with_a_table_so_large_that_costs_are_counted_coarsely():
+    # 2^27 positions per sequence and 12000 rows of 64 heads: the costs of the units could pass 31 bits
+    b = ref.Batch([300, 2000], [12000, 40], 8, 64, 64, seed=6)
+    table = torch.full((2, 1 << 24), -7, dtype=torch.int32, device="cuda")
+    table[:, :b.table.shape[1]] = b.table
+    got, lse = attn.cached(b.q, b.k_pages, b.v_pages, table, b.cu_rows, b.kv_lens, want_lse=True)
+    ok()
+    check_attention(b, 0, got, lse)
+
+
+def test_append_and_attention_past_four_gigabytes_of_pages():
+    pages, heads, page = 9000, 16, 256  # 4.7 GB of keys
+    k_pages, v_pages = (torch.empty(pages, heads, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kv, g = 700, torch.Generator(device="cuda").manual_seed(3)
+    k, v, q = (torch.randn(kv, heads, D, generator=g, device="cuda").bfloat16() for _ in range(3))
+    table = i32([[pages - 1, 0, pages - 3, 5]])
+    t = torch.arange(kv, device="cuda")
+    slots = (table[0, t // page].long() * page + t % page).int()
+    attn.cache_append(k, v, slots, k_pages, v_pages)
+    got = attn.cached(q[-20:], k_pages, v_pages, table, i32([0, 20]), i32([kv]), causal_unit=1)
+    ok()
+    want, _, spread = ref.attention(q[-20:], [k], [v], [0, 20], [kv], 1)
+    assert ((got.double() - want).abs() <= 2.0 ** -8 * (1.01 * want.abs() + 1.12 * spread) + 1e-30).all()
+
+
+def test_norm_past_two_to_the_31_elements():
+    rows, cols = 270000, 8192
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, cols, device="cuda").bfloat16()
+    _, h = attn.norm_residual(x, eps=1e-6)
+    ok()
+    want = ref.normed(x[-3:].double(), "layer", 1e-6, None, None)
+    assert ((h[-3:].double() - want).abs() <= norm_tolerance(2, "layer", 1e-6, want, torch.bfloat16)).all()
+    assert (h[:3] == 0).all()
+
+
 def test_calls_without_rows():
     b = ref.Batch([40, 0], [0, 0], 16, 4, 2, seed=2)
     got, lse = attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, want_lse=True)
