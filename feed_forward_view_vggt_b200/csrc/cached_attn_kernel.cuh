@@ -61,9 +61,12 @@ namespace vggt {
 
 constexpr int kMaxCtas = 148;
 // Of every 16 column pairs of a score row, those whose exponentials are a
-// polynomial (see attn_fwd_kernel, which takes 4).  Measured, one frame over
-// 100 cached: 0: 967 us, 1: 973, 2: 959, 3: 948, 4: 969, 5: 1060, 6: 1160.
-constexpr int kCachedPolyPairs = 3;
+// polynomial (see attn_fwd_kernel).  Its argument is cut at 127 from above too:
+// against the old offset a later tile's may be hundreds, and 2^j has no exponent
+// bits then; cut, P is so large that the tile is done again.  Measured, one
+// frame over 100 cached: 0 pairs 952 us, 1: 944, 2: 940, 3: 971.
+constexpr int kCachedPolyPairs = 2;
+constexpr float kExp2MaxArg = 127.0f;
 constexpr int kTaskRing = 8;
 // What a unit costs beside its steps (Q load, first score, epilogue), in
 // steps, and the fewest steps a CTA is used for.  Measured over fourteen small
@@ -1141,7 +1144,8 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
                             float a, b;
                             f2_unpack(x2, a, b);
                             if (e < kCachedPolyPairs) {
-                                const uint64_t xc = f2_pack(fmaxf(a, kExp2MinArg), fmaxf(b, kExp2MinArg));
+                                const uint64_t xc = f2_pack(fminf(fmaxf(a, kExp2MinArg), kExp2MaxArg),
+                                                            fminf(fmaxf(b, kExp2MinArg), kExp2MaxArg));
                                 const uint64_t y = f2_add(xc, magic2);
                                 const uint64_t jj = f2_add(y, neg_magic2);
                                 const uint64_t f = f2_fma(jj, neg_one2, xc);
