@@ -88,7 +88,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE,
            "-o", tmp, BINDING_SOURCE, "-L", os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
-           "-ltorch_python"]
+           "-ltorch_cuda", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)

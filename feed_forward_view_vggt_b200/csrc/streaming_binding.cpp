@@ -10,6 +10,8 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -80,6 +82,7 @@ F *entry(PyObject *address)
 // on the current stream may still be in use on it.  What is returned is freed
 // only after the work of the current stream that reads it.
 struct Call {
+    at::AutoDispatchBelowADInplaceOrView below_autograd;  // results are plain tensors: no view or gradient to track
     c10::cuda::CUDAGuard device;
     c10::cuda::CUDAStream current;
     std::optional<c10::cuda::CUDAStream> other;
@@ -115,13 +118,12 @@ struct Call {
 
     at::Tensor empty(at::IntArrayRef shape, ScalarType type, bool returned = true) const
     {
-        const auto options = at::TensorOptions().dtype(type).device(current.device());
         if (!other)
-            return at::empty(shape, options);
+            return at::detail::empty_cuda(shape, type, current.device(), std::nullopt);
         at::Tensor t;
         {
             const c10::cuda::CUDAStreamGuard guard(*other);
-            t = at::empty(shape, options);
+            t = at::detail::empty_cuda(shape, type, current.device(), std::nullopt);
         }
         if (returned)
             c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current);
