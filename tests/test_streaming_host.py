@@ -173,6 +173,16 @@ def test_binding_checks_its_tensors():
         attn.norm_residual(torch.zeros(2, 8), gate=torch.zeros(2, 8), rows_per_gate=2)
 
 
+def test_binding_says_when_its_module_is_not_built(monkeypatch):
+    import sys
+
+    monkeypatch.setattr(attn, "_host", None)
+    monkeypatch.setitem(sys.modules, "feed_forward_view_vggt_b200._streaming", None)
+    monkeypatch.delattr(sys.modules["feed_forward_view_vggt_b200"], "_streaming", raising=False)
+    with pytest.raises(RuntimeError, match="not built"):
+        attn.norm_residual(torch.zeros(2, 8))
+
+
 def test_the_references_agree_with_hand_values():
     # two keys, logits 0 and ln 3: weights 1/4 and 3/4; the first row sees the first key alone
     q = torch.zeros(2, 1, 64)
