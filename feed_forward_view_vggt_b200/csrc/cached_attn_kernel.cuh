@@ -34,8 +34,8 @@
 // after PV(k) are those of attn_fwd_kernel.
 //
 // Bound by the exponentials and the instructions around them, as that kernel
-// is: one frame of 1374 tokens over 100 cached ones, 16 heads, 0.94 ms or 830
-// TFLOP/s alone, 1.07 ms or 730 in a row under the power cap.  Single tokens are
+// is: one frame of 1374 tokens over 100 cached ones, 16 heads, 0.89 ms or 870
+// TFLOP/s alone, 1.04 ms or 750 in a row under the power cap.  Single tokens are
 // bound by HBM: 148 sequences of 32000 keys 6.9 TB/s, 48 of odd lengths in pages
 // of 16, with grouped heads, 178 us or 4.8 TB/s.  Small calls are bound by
 // latency: planning 0.8 us, finding the first task 1.2 us, first keys 1.5 us,
@@ -110,6 +110,7 @@ struct Task {
     int b, hk;
     int kind, slot;     // slot of the workspace, -1: the whole unit
     int vlast;          // keys of the last tile that exist, 1..128
+    int rot;            // the j-th tile worked on is (j + rot) mod n
 };
 
 struct __align__(1024) CachedSmem {
@@ -325,7 +326,7 @@ __device__ __forceinline__ bool load_task(CachedSmem &sm, const CUtensorMap *tmQ
     const uint32_t box_bytes = static_cast<uint32_t>(p.box_rows) * kHeadDim * 2;
     const uint32_t full = smem_u32(kIsV ? sm.v_full : sm.k_full), empty = smem_u32(kIsV ? sm.v_empty : sm.k_empty);
     const uint32_t tiles = smem_u32(kIsV ? sm.v[0] : sm.k[0]);
-    const int n = t.n, hk = t.hk, kt0 = t.kt0, vlast = t.vlast;
+    const int n = t.n, hk = t.hk, kt0 = t.kt0, vlast = t.vlast, rot = t.rot;
     const int32_t *table = p.table + static_cast<int64_t>(t.b) * p.max_pages;
     if (!kIsV) {
         const uint32_t qb = issued.q & 1u, q_bytes = static_cast<uint32_t>(p.group * p.tile_tokens) * kHeadDim * 2;
@@ -343,10 +344,10 @@ __device__ __forceinline__ bool load_task(CachedSmem &sm, const CUtensorMap *tmQ
     }
     // Page of this lane's box of tile j; the first key of the box exists.
     auto lookup = [&](int j) -> int {
-        const int valid = j == n - 1 ? vlast : kBlockN;
+        const int r = j + rot < n ? j + rot : j + rot - n, valid = r == n - 1 ? vlast : kBlockN;
         if (lane * p.box_rows >= valid)
             return 0;
-        const int page = __ldg(table + p.by_page.div((kt0 + j) * kBlockN + lane * p.box_rows));
+        const int page = __ldg(table + p.by_page.div((kt0 + r) * kBlockN + lane * p.box_rows));
         if (page >= 0 && page < p.n_pages)
             return page;
         record_bounds_failure(kCheckCachePage);
@@ -354,9 +355,9 @@ __device__ __forceinline__ bool load_task(CachedSmem &sm, const CUtensorMap *tmQ
     };
     int page = lookup(0);
     for (int j = 0; j < n; ++j) {
-        const int valid = j == n - 1 ? vlast : kBlockN;
+        const int r = j + rot < n ? j + rot : j + rot - n, valid = r == n - 1 ? vlast : kBlockN;
         const int boxes = (valid + p.box_rows - 1) / p.box_rows;
-        const int key = (kt0 + j) * kBlockN + lane * p.box_rows, off = key - p.by_page.div(key) * p.page_size;
+        const int key = (kt0 + r) * kBlockN + lane * p.box_rows, off = key - p.by_page.div(key) * p.page_size;
         const int here = page;
         if (j + 1 < n)
             page = lookup(j + 1);
@@ -389,7 +390,12 @@ __device__ __forceinline__ void drain_copies(CachedSmem &sm, const Issued &issue
 }
 
 // Warp 0: walks along the CTA's part of the work, hands on its tasks, then one
-// with n = 0 that ends the list, and loads their Q and K tiles.  V is warp 3's:
+// with n = 0 that ends the list, and loads their Q and K tiles.  It walks from
+// the end, and a task's tiles may be taken in a rotated order: a head's CTAs,
+// whose shares start at different keys, then read about the same keys at the
+// same time, and its K and V leave DRAM fewer times: one frame over 100 cached
+// reads 1.35 GB instead of 3.15 (0.56 are needed), 894 us instead of 938 alone and
+// 1039 instead of 1110 in a row, where the power cap sets the clock.  V is warp 3's:
 // the copies of a tile of small pages are many (16 of 2 KB for pages of 16),
 // and a warp issues those of its lanes one after another.  Units without keys (their sequence was
 // refused pages, e.g.) are dealt with here and never enter the ring.
@@ -405,11 +411,12 @@ __device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ
     const int each = work / ctas, rest = work - each * ctas;
     auto start = [&](int i) { return i * each + i * rest / ctas; };
     Join join{0, 0, 0, 0};
-    int w = 0, w1 = 0;
+    int w0 = 0, w = 0;  // the share's first point, and the end of what is left of it
     if (cta < ctas) {
-        w = start(cta);
-        w1 = start(cta + 1);
+        w0 = start(cta);
+        w = start(cta + 1);
     }
+    int now = 0;  // tiles of a pair that took as long as the work so far
     uint32_t it = 0;
     auto push = [&](const Task &t) -> bool {
         const uint32_t slot = it % kTaskRing;
@@ -423,13 +430,13 @@ __device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ
         ++it;
         return t.n == 0 || load_task<false>(sm, tmQ, tmK, p, t, issued);
     };
-    while (w < w1) {
-        // The sequence, head and unit at point w, and x, its place in the unit.
-        const int b = upper_bound(sm.work_end, p.n_seqs, w);
+    while (w > w0) {
+        // The sequence, head and unit of the last point, and x, its place in the unit.
+        const int at = w - 1, b = upper_bound(sm.work_end, p.n_seqs, at);
         const int first = b ? sm.work_end[b - 1] : 0, per_head = (sm.work_end[b] - first) / p.Hkv;
         const Seq s = load_seq(p, b);
         const int units = unit_count(p, s);
-        int hk = (w - first) / per_head, x = w - first - hk * per_head, i = 0;
+        int hk = (at - first) / per_head, x = at - first - hk * per_head, i = 0;
         for (;; i += 32) {
             const int cost = i + lane < units ? unit_of(p, s, i + lane).cost : 0;
             int upto = cost;
@@ -441,26 +448,28 @@ __device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ
             }
             const unsigned over = __ballot_sync(0xffffffffu, upto > x);
             if (over || i + 32 >= units) {
-                const int at = over ? __ffs(over) - 1 : 31;
-                x -= __shfl_sync(0xffffffffu, upto - cost, at);
-                i += at;
+                const int in = over ? __ffs(over) - 1 : 31;
+                x -= __shfl_sync(0xffffffffu, upto - cost, in);
+                i += in;
                 break;
             }
             x -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        while (w < w1 && hk < p.Hkv) {
+        int x1 = x + 1;  // end of the share in the unit
+        while (w > w0 && hk >= 0) {
             const Unit u = unit_of(p, s, i);
-            const int x1 = min(u.cost, x + w1 - w);
+            x1 = x1 > 0 ? x1 : u.cost;
+            const int x0 = max(0, x1 - (w - w0));
             Task t;
             t.row0 = s.row0 + 2 * i * p.tile_tokens;
             t.row_end = s.row0 + s.n;
             t.hk = hk;
             t.kind = u.kind;
             if (u.tiles == 0) {
-                if (x == 0)
+                if (x0 == 0)
                     write_empty_rows(p, t.row0, t.row_end, t.kind, t.hk);
             } else {
-                t.kt0 = tiles_before(p, u, x);
+                t.kt0 = tiles_before(p, u, x0);
                 t.n = tiles_before(p, u, x1) - t.kt0;
                 t.b = b;
                 t.pos0 = s.kv - (t.row_end - t.row0);
@@ -471,7 +480,7 @@ __device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ
                     t.slot = 2 * cta + (t.kt0 == 0);
                     if (t.kt0 == 0) {
                         // up to the CTA that has the unit's last point
-                        const int end = w - x + u.cost;
+                        const int end = w - x1 + u.cost;
                         int last = min(ctas - 1, static_cast<int>(static_cast<float>(end) * ctas / work) + 1);
                         while (last > cta && start(last) >= end)
                             --last;
@@ -481,14 +490,23 @@ __device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ
                         join.parts = last - cta + 1;
                     }
                 }
+                // Where every row sees every key of the task, its tiles are taken
+                // in the order that brings tile `now` of the head at time `now`.
+                t.rot = 0;
+                if (t.kind != kTaskFew && key_limit(p, t.kv, t.pos0) >= min(t.kv, (t.kt0 + t.n) * kBlockN)) {
+                    const int ahead = now - t.kt0;
+                    if (ahead > -t.n && ahead < t.n)
+                        t.rot = ahead >= 0 ? ahead : ahead + t.n;
+                }
                 if (t.n > 0 && !push(t))
                     return;
+                now += t.kind == kTaskPair ? t.n : t.n >> 1;
             }
-            w += x1 - x;
-            x = 0;
-            if (++i == units) {
-                i = 0;
-                ++hk;
+            w -= x1 - x0;
+            x1 = 0;
+            if (--i < 0) {
+                i = units - 1;
+                --hk;
             }
         }
     }
@@ -587,7 +605,7 @@ __device__ __forceinline__ void issue_loop(CachedSmem &sm, uint32_t tmem)
         if (!wait_task(sm, it))
             return;
         const Task &t = sm.task[it % kTaskRing];
-        const int n = t.n, kind = t.kind, kk_last = (t.vlast + 15) >> 4;
+        const int n = t.n, kind = t.kind, kk_last = (t.vlast + 15) >> 4, last_at = n - 1 - t.rot;
         release_task(sm, it);
         if (n == 0)
             return;
@@ -605,7 +623,7 @@ __device__ __forceinline__ void issue_loop(CachedSmem &sm, uint32_t tmem)
         if (!fews_over())
             return;
         const bool pair = kind == kTaskPair;
-        const int steps = pair ? 2 * n : n, last_tile = pair ? steps - 2 : steps - 1;
+        const int steps = pair ? 2 * n : n;
         const uint32_t qb = static_cast<uint32_t>(it) & 1u;
         if (!kIsPV && !wait_bar(smem_u32(&sm.q_full[qb]), (static_cast<uint32_t>(it) >> 1) & 1u, ab, kSiteQFull))
             return;
@@ -624,7 +642,7 @@ __device__ __forceinline__ void issue_loop(CachedSmem &sm, uint32_t tmem)
                 tc_fence_after();
                 const uint32_t d = tmem + kTmemO + wg * kHeadDim;
                 umma_ts(d, scores, b, kIdesc, s >= 2 ? 1u : 0u);
-                if (s < last_tile) {
+                if ((pair ? s >> 1 : s) != last_at) {
 #pragma unroll
                     for (int kk = 1; kk < kBlockN / 16; ++kk)
                         umma_ts(d, scores + 8 * kk, b + 128 * kk, kIdesc, 1u);
@@ -1077,14 +1095,15 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
 
         uint32_t k = k0 + static_cast<uint32_t>(wg);  // the step, mod 6
         for (int x = 0; x < steps; ++x) {
-            const int j = w.kind == kTaskPair ? x : 2 * x + wg;  // key tile within the task
+            const int j = w.kind == kTaskPair ? x : 2 * x + wg;
+            const int tile = j + w.rot < w.n ? j + w.rot : j + w.rot - w.n;  // key tile within the task
             if (k >= 6)
                 k -= 6;
             const uint32_t buf = k >= 3 ? k - 3 : k;
             const uint32_t tS = tmem + buf * kBlockN + lane_off;
             if (!wait_step(bar_s + 8 * turn.slot, turn.ph, ab, kSiteSFull))
                 return;
-            if (j == w.n - 1 && (w.vlast & 15) != 0 && (w.kind != kTaskPair || wg == 0)) {
+            if (tile == w.n - 1 && (w.vlast & 15) != 0 && (w.kind != kTaskPair || wg == 0)) {
                 // V rows behind the last key, up to the end of its group of 16
                 const uint32_t u = ring + static_cast<uint32_t>(j), st = u % kStages;
                 if (!wait_bar_warp(smem_u32(&sm.v_full[st]), (u / kStages) & 1, ab, kSiteVFull))
@@ -1104,8 +1123,8 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     reg_fence(s[i]);
-                const int valid = lim - j * kBlockN;
-                if (warp_lim < (j + 1) * kBlockN) {
+                const int valid = lim - tile * kBlockN;
+                if (warp_lim < (tile + 1) * kBlockN) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
 #pragma unroll

@@ -181,6 +181,18 @@ def test_attention_matches_64_bits(case):
     assert (got[b.cu[-1]:] == 9.0).all()  # rows behind the last sequence
 
 
+@pytest.mark.parametrize("kv,new,heads,kv_heads,unit", [([20003], [1374], 16, 16, 0), ([20003], [1374], 16, 16, 1),
+                                                        ([9001, 5000], [1000, 641], 16, 4, 0),
+                                                        ([9001, 5000], [1000, 641], 16, 4, 641)])
+def test_attention_when_shares_are_long(kv, new, heads, kv_heads, unit):
+    """Every CTA has many key tiles of several units and takes them in an order of its own, the odd last tile in
+    between."""
+    b = ref.Batch(kv, new, 64, heads, kv_heads, seed=12)
+    got, lse = attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, causal_unit=unit, want_lse=True)
+    ok()
+    check_attention(b, unit, got, lse)
+
+
 @pytest.mark.parametrize("heads,kv_heads,unit,seed", [(16, 8, 1, 1), (4, 4, 0, 2), (16, 1, 30, 3), (21, 3, 1, 4)])
 def test_attention_of_many_sequences_of_every_kind(heads, kv_heads, unit, seed):
     """Several hundred sequences, so that every CTA works through many tasks: single tokens, a few rows, one tile,
