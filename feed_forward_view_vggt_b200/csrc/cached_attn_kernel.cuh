@@ -64,7 +64,8 @@ constexpr int kMaxCtas = 148;
 // polynomial (see attn_fwd_kernel).  Its argument is cut at 127 from above too:
 // against the old offset a later tile's may be hundreds, and 2^j has no exponent
 // bits then; cut, P is so large that the tile is done again.  Measured, one
-// frame over 100 cached: 0 pairs 952 us, 1: 944, 2: 940, 3: 971.
+// frame over 100 cached: 1 pair 905 us, 2: 907, 3: 983; over 32, in a row: 1
+// 344 us, 2: 341.
 constexpr int kCachedPolyPairs = 2;
 constexpr float kExp2MaxArg = 127.0f;
 constexpr int kTaskRing = 8;
@@ -1150,7 +1151,7 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
                 // before it is rounded (see attn_fwd_kernel for the split of
                 // the exponentials between the MUFU unit and a polynomial).
                 auto exp_tile = [&]() -> float {
-                    const float base = m == -INFINITY ? 0.f : m;  // a row that sees nothing: P = 0
+                    const float base = fmaxf(m, -1e30f);  // a row that sees nothing: P = 0
                     const uint64_t neg_m2 = f2_pack(-base, -base);
                     uint64_t ls[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
@@ -1360,10 +1361,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // 168 registers/thread at launch; 128 x (72 + 216 + 216) = 384 x 168.
     if (warp < 4) {
         setmaxnreg_dec<kRegsControl>();
-        // The order of the roles is that of their code.  The loops that run
-        // together (issuers, softmax) stand side by side; with the issuers first
-        // one frame over 100 cached takes 1050 us, in the order of the warps 990,
-        // in this one 945 (instruction fetch stalls).
+        // The order of the roles is that of their code: the loops that run
+        // together (issuers, softmax) stand side by side.
         if (warp == 0)
             run_k_producer(sm, &tmQ, &tmK, p);
         else if (warp == 3)
