@@ -56,10 +56,10 @@
 #include "cache_kernels.cuh"
 #include "device_error.cuh"
 #include "ptx.cuh"
+#include "shares.cuh"
 
 namespace vggt {
 
-constexpr int kMaxCtas = 148;
 // Of every 16 column pairs of a score row, those whose exponentials are a
 // polynomial (see attn_fwd_kernel).  Its argument is cut at 127 from above too:
 // against the old offset a later tile's may be hundreds, and 2^j has no exponent
@@ -69,18 +69,11 @@ constexpr int kMaxCtas = 148;
 constexpr int kCachedPolyPairs = 2;
 constexpr float kExp2MaxArg = 127.0f;
 constexpr int kTaskRing = 8;
-// What a unit costs beside its steps (Q load, first score, epilogue), in
-// steps, and the fewest steps a CTA is used for.  Measured over fourteen small
-// and middle calls, geometric mean: (1, 4) for the last two 20.3 us, (3, 4)
-// 19.1, (3, 3) 18.8, (3, 2) 18.9, (1, 1) 19.5, (6, 4) 19.1; 3, 10 and 16 for the
-// first within 0.3% of 6.
-constexpr int kUnitCost = 6, kFewUnitCost = 3, kMinSteps = 3;
 
 constexpr int kFewRows = 16;      // rows of a task that the warps work on by themselves
 constexpr int kSoftmaxWarps = 8;  // and with how many: 16 keys of a tile each
 
 enum : uint32_t { kSiteTaskFull = 12, kSiteTaskEmpty, kSiteMergeReady, kSiteMergeFree, kSiteFewQ, kSiteFewFull, kSiteTaskPassed };
-enum : int { kTaskSingle = 0, kTaskPair = 1, kTaskFew = 2 };
 
 // What a CTA leaves for the joining launch: the unit whose first part, but not
 // its last, was its work.  Parts 1, 2, ... are those of the CTAs behind it.
@@ -196,18 +189,8 @@ __device__ __forceinline__ Unit unit_of(const CachedParams &p, const Seq &s, int
     const int left = s.n - 2 * i * p.tile_tokens;
     u.kind = left > p.tile_tokens ? kTaskPair : (left * p.group <= kFewRows ? kTaskFew : kTaskSingle);
     u.tiles = pair_tiles(p, s, i);
-    const int steps = (u.kind == kTaskPair ? 2 * u.tiles : u.tiles) + (u.kind == kTaskFew ? kFewUnitCost : kUnitCost);
-    u.cost = u.tiles == 0 ? 1 : ((steps - 1) >> p.cost_shift) + 1;
+    u.cost = unit_points(u.kind, u.tiles, p.cost_shift);
     return u;
-}
-
-// Key tiles of a unit before point x of its cost.
-__device__ __forceinline__ int tiles_before(const CachedParams &p, const Unit &u, int x)
-{
-    int steps = (x << p.cost_shift) - (u.kind == kTaskFew ? kFewUnitCost : kUnitCost);
-    if (u.kind == kTaskPair)
-        steps >>= 1;
-    return max(0, min(steps, u.tiles));
 }
 
 // Sums the costs: work_end and work.  Every thread takes a run of consecutive
@@ -404,18 +387,12 @@ __device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ
                                           const CachedParams &p, Issued &issued)
 {
     const int lane = threadIdx.x & 31, cta = static_cast<int>(blockIdx.x);
-    const int work = sm.work;
-    const int ctas = work >= kMaxCtas * kMinSteps
-                         ? static_cast<int>(gridDim.x)
-                         : max(1, min(static_cast<int>(gridDim.x), (work << p.cost_shift) / kMinSteps));
-    // CTA i starts at floor(i * work / ctas)
-    const int each = work / ctas, rest = work - each * ctas;
-    auto start = [&](int i) { return i * each + i * rest / ctas; };
+    const Shares shares(sm.work, p.cost_shift, static_cast<int>(gridDim.x));
     Join join{0, 0, 0, 0};
     int w0 = 0, w = 0;  // the share's first point, and the end of what is left of it
-    if (cta < ctas) {
-        w0 = start(cta);
-        w = start(cta + 1);
+    if (cta < shares.ctas) {
+        w0 = shares.start(cta);
+        w = shares.start(cta + 1);
     }
     int now = 0;  // tiles of a pair that took as long as the work so far
     uint32_t it = 0;
@@ -470,8 +447,8 @@ __device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ
                 if (x0 == 0)
                     write_empty_rows(p, t.row0, t.row_end, t.kind, t.hk);
             } else {
-                t.kt0 = tiles_before(p, u, x0);
-                t.n = tiles_before(p, u, x1) - t.kt0;
+                t.kt0 = tiles_before(u.kind, u.tiles, x0, p.cost_shift);
+                t.n = tiles_before(u.kind, u.tiles, x1, p.cost_shift) - t.kt0;
                 t.b = b;
                 t.pos0 = s.kv - (t.row_end - t.row0);
                 t.kv = s.kv;
@@ -481,14 +458,10 @@ __device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ
                     t.slot = 2 * cta + (t.kt0 == 0);
                     if (t.kt0 == 0) {
                         // up to the CTA that has the unit's last point
-                        const int end = w - x1 + u.cost;
-                        int last = min(ctas - 1, static_cast<int>(static_cast<float>(end) * ctas / work) + 1);
-                        while (last > cta && start(last) >= end)
-                            --last;
                         join.row0 = t.row0;
                         join.rows = min(t.row_end - t.row0, 2 * p.tile_tokens) * p.group;
                         join.hk = hk;
-                        join.parts = last - cta + 1;
+                        join.parts = shares.last(cta, w - x1 + u.cost) - cta + 1;
                     }
                 }
                 // Where every row sees every key of the task, its tiles are taken

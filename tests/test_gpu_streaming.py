@@ -300,6 +300,40 @@ def test_attention_with_a_table_so_large_that_costs_are_counted_coarsely():
     check_attention(b, 0, got, lse)
 
 
+@pytest.mark.parametrize("active", [{0: 300}, {4000: 600}, {17: 2000}, {5: 300, 4095: 2000}, {0: 600, 1: 300}])
+@pytest.mark.parametrize("heads,kv_heads,new", [(16, 16, 1), (64, 16, 200)])
+def test_attention_of_little_work_in_buffers_of_full_size(active, heads, kv_heads, new):
+    """4096 sequences in a table for 2^22 positions, a few of them active: costs are counted in fours of steps and
+    there are fewer of those than CTAs.  What the workspace held before must not reach a result."""
+    seqs, rows, page, width = 4096, 4096, 1 << 17, 32
+    g = torch.Generator(device="cuda").manual_seed(4)
+    k_pages, v_pages = (torch.full((len(active), kv_heads, page, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+                        for _ in range(2))
+    q = torch.randn(rows, heads, D, generator=g, device="cuda").bfloat16()
+    kv, fresh = [0] * seqs, [0] * seqs
+    ks, vs = [], []
+    table = torch.full((seqs, width), -7, dtype=torch.int32, device="cuda")
+    for i, (b, n) in enumerate(active.items()):
+        kv[b], fresh[b] = n, new
+        k_pages[i, :, :n] = torch.randn(kv_heads, n, D, generator=g, device="cuda").bfloat16()
+        v_pages[i, :, :n] = torch.randn(kv_heads, n, D, generator=g, device="cuda").bfloat16()
+        ks.append(k_pages[i, :, :n].transpose(0, 1))
+        vs.append(v_pages[i, :, :n].transpose(0, 1))
+        table[b, 0] = i
+    cu = np.concatenate([[0], np.cumsum(fresh)]).tolist()
+    cache = attn.vggt_cache(seqs, heads, kv_heads, D, page, len(active), width, *k_pages.stride()[:3])
+    ws = torch.empty(attn.vggt_attn_cached_workspace_bytes(cache, rows), dtype=torch.uint8, device="cuda")
+    ends = [new * i for i in range(len(active) + 1)]
+    want, _, spread = ref.attention(q, ks, vs, ends, list(active.values()), 1)
+    for fill in (0xff, 0x7f):  # NaN, and 3e38
+        ws.fill_(fill)
+        got = attn.cached(q, k_pages, v_pages, table, i32(cu), i32(kv), causal_unit=1, workspace=ws)
+        ok()
+        n = cu[-1]
+        tol = 2.0 ** -8 * (1.01 * want.abs() + 1.12 * spread) + 1e-30
+        assert ((got.double() - want).abs() <= tol)[:n].all()
+
+
 def test_append_and_attention_past_four_gigabytes_of_pages():
     pages, heads, page = 9000, 16, 256  # 4.7 GB of keys
     k_pages, v_pages = (torch.empty(pages, heads, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
