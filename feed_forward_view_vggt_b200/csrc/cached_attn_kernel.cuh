@@ -67,7 +67,6 @@ namespace vggt {
 // frame over 100 cached: 1 pair 905 us, 2: 907, 3: 983; over 32, in a row: 1
 // 344 us, 2: 341.
 constexpr int kCachedPolyPairs = 2;
-constexpr float kExp2MaxArg = 127.0f;
 constexpr int kTaskRing = 8;
 
 constexpr int kFewRows = 16;      // rows of a task that the warps work on by themselves
