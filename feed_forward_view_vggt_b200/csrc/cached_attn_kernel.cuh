@@ -869,7 +869,8 @@ __device__ __forceinline__ bool run_few(CachedSmem &sm, const CachedParams &p, c
                 top[e] = fmax3(s[0][2 * e], s[0][2 * e + 1], s[1][2 * e]);
                 top[e] = fmax3(top[e], s[1][2 * e + 1], s[2][2 * e]);
                 top[e] = fmax3(top[e], s[2][2 * e + 1], s[3][2 * e]);
-                top[e] = fmaxf(top[e], s[3][2 * e + 1]) * sl2;
+                // a row of no token has no say in when the offsets move
+                top[e] = g + 8 * e < rows ? fmaxf(top[e], s[3][2 * e + 1]) * sl2 : -INFINITY;
             }
             // The offset moves when a logit passes it by kRescaleThreshold
             // (P <= 2^8), so most tiles need no maximum over the lanes.
@@ -1169,9 +1170,11 @@ __device__ __forceinline__ void run_cached_softmax(CachedSmem &sm, uint32_t tmem
                 if (x == 0)
                     m = tile_max();
                 float tsum = exp_tile();
-                if (x > 0 && __any_sync(0xffffffffu, !(tsum <= kTileSumLimit))) {
+                // Rows of no token of the task have no say: whether a row below
+                // the limit moves its offset too would hang on their contents.
+                if (x > 0 && __any_sync(0xffffffffu, row_ok && !(tsum <= kTileSumLimit))) {
                     const float cand = tile_max();
-                    const bool need = cand > m + kRescaleThreshold;
+                    const bool need = row_ok && cand > m + kRescaleThreshold;
                     if (__any_sync(0xffffffffu, need)) {
                         // this warpgroup's last PV: step k - 2
                         const uint32_t before = k >= 2 ? k - 2 : k + 4;

@@ -265,6 +265,31 @@ def test_attention_when_one_late_key_outweighs_all(new, alike, at):
     check_attention(b, 0, got, lse, logit_error=64 * 2.0 ** -24 * most)
 
 
+@pytest.mark.parametrize("kv,new,kv_heads", [([5000], [1], 1), ([3000, 2500], [1, 3], 1), ([20000], [50], 16),
+                                             ([20000], [8], 16), ([9000, 12000], [130, 50], 16), ([5000], [5], 1)])
+def test_attention_does_not_depend_on_rows_of_no_sequence(kv, new, kv_heads):
+    """Groups of 3: a tile holds rows of other tokens and rows of no token.  Whatever q holds behind the last
+    sequence, and whatever an earlier call left in shared memory, the sequences' results keep their bits."""
+    b = ref.Batch(kv, new, 16, 3 * kv_heads, kv_heads, seed=14, pad=60)
+    for i, n in enumerate(kv):  # keys that grow along every thousand, so the offsets move
+        ramp = 0.05 + 2.95 * (torch.arange(n, device="cuda") % 1000) / 1000
+        b.k_seqs[i] = (b.k_seqs[i] * ramp[:, None, None]).bfloat16()
+        table = b.table[i].tolist()
+        for page in range(-(-n // 16)):
+            part = b.k_seqs[i][16 * page:16 * page + 16]
+            b.k_pages[table[page], :, :len(part)] = part.transpose(0, 1)
+    call = lambda: attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens)  # noqa: E731
+    b.q[b.cu[-1]:] = 0
+    want = call()
+    ok()
+    check_attention(b, 0, want)
+    unlike = torch.randn(60, 3 * kv_heads, D, generator=torch.Generator().manual_seed(1)).cuda()
+    for fill in (30 * unlike, 3000 * unlike, torch.full_like(unlike, float("nan"))):
+        b.q[b.cu[-1]:] = fill.bfloat16()
+        assert torch.equal(call()[:b.cu[-1]], want[:b.cu[-1]])
+    ok()
+
+
 def test_attention_skips_and_reports_a_page_outside_the_cache():
     b = ref.Batch([400, 300], [3, 4], 16, 2, 2, seed=2)
     good = attn.cached(b.q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens)
