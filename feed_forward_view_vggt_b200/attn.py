@@ -14,6 +14,7 @@ non-zero status.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -600,6 +601,12 @@ def _torch():
     return torch
 
 
+def _torch_stream(stream, device):
+    """``stream``, as the calls take it, as one of torch's."""
+    cuda = _torch().cuda
+    return stream if isinstance(stream, cuda.Stream) else cuda.ExternalStream(_stream(stream), device=device)
+
+
 def _expect(ok, what):
     if not ok:
         raise ValueError(what)
@@ -614,7 +621,7 @@ def cache_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size
     if n_pages is None:
         n_pages = (2 ** 31 - 1) // page_size if page_size > 0 else 1
     return _call("vggt_cache_plan", "plan", cached_lens, new_lens, free_pages, n_free, block_table, page_size, n_rows,
-                 n_pages, stream)[1:]
+                 n_pages, stream, None, None)[1:]
 
 
 def cache_append(k, v, slots, k_pages, v_pages, stream=None):
@@ -649,7 +656,12 @@ class PagedCache:
     that share one block table, the sequences' lengths and the free list, all
     on the device.  A step is ``plan(new_lens, n_rows)``, then per layer
     ``append(layer, k, v)`` and ``attend(layer, q)``, with the rows of the
-    sequences packed one after another."""
+    sequences packed one after another.
+
+    Everything stays where it is: ``plan`` updates the lengths in place, and
+    two plans with the same n_rows write the same ``cu_rows`` and ``slots``.  A
+    step may therefore be captured into a graph, with its plan or only its
+    layers; every replay goes on from the cache's present state."""
 
     def __init__(self, n_pages, page_size, n_kv_heads, n_seqs, max_pages, n_layers=1, head_dim=64, device=None):
         import torch
@@ -661,29 +673,51 @@ class PagedCache:
         self.pages = [tuple(torch.zeros(n_pages, n_kv_heads, page_size, head_dim, dtype=torch.bfloat16, device=device)
                             for _ in range(2)) for _ in range(n_layers)]
         self.block_table = torch.full((n_seqs, max_pages), -1, **i32)
-        self.kv_lens = torch.zeros(n_seqs, **i32)
+        # of the last step: free pages, sequences refused, and the sequences' lengths
+        self._state = torch.zeros(2 + n_seqs, **i32)
+        self._state[0] = n_pages
+        self.n_free, self.kv_lens = self._state[:1], self._state[2:]
         # one entry more than the pages: where release() drops what it must not write
         self.free_pages = torch.arange(n_pages + 1, **i32)
-        self.n_free = torch.full((1,), n_pages, **i32)
+        self._free = self.free_pages[:n_pages]
         self.cu_rows = self.slots = None
+        self._steps = {}  # by rows, rounded up to a power of two: a step's row offsets and slots
 
     def plan(self, new_lens, n_rows, stream=None):
         """Plans a step of new_lens rows (int32 [n_seqs], on the device) in buffers of n_rows rows; returns the
         number of refused sequences (int32 [1], on the device)."""
-        n_pages = self.pages[0][0].shape[0]
-        self.cu_rows, self.kv_lens, self.slots, counts = cache_plan(
-            self.kv_lens, new_lens, self.free_pages[:n_pages], self.n_free, self.block_table, self.page_size, n_rows,
-            n_pages=n_pages, stream=stream)
-        self.n_free = counts[:1]
+        size = 1 << max(int(n_rows) - 1, 0).bit_length()
+        step, device = self._steps.get(size), self._state.device
+        if step is None:
+            # on the call's stream: memory that the current one has freed may still be in use on it
+            with _torch().cuda.stream(None if stream is None else _torch_stream(stream, device)):
+                step = self._steps[size] = self._state.new_empty(self.kv_lens.numel() + 1 + size)
+        _, self.cu_rows, _, self.slots, counts = _call(
+            "vggt_cache_plan", "plan", self.kv_lens, new_lens, self._free, self.n_free, self.block_table,
+            self.page_size, n_rows, self.pages[0][0].shape[0], stream, step, self._state)
+        if stream is not None:
+            self._used_on(stream, self._state, self.free_pages, self.block_table)
+            step.record_stream(_torch().cuda.current_stream(device))
         return counts[1:]
+
+    def _used_on(self, stream, *tensors):
+        """When the cache goes, these and its step buffers are given to nobody before ``stream`` is past its work."""
+        if stream is not None:
+            stream = _torch_stream(stream, self.kv_lens.device)
+            for t in (*tensors, *self._steps.values()):
+                t.record_stream(stream)
 
     def append(self, layer, k, v, stream=None):
         """Writes the step's rows of a layer."""
         cache_append(k, v, self.slots, *self.pages[layer], stream=stream)
+        self._used_on(stream, *self.pages[layer])
 
-    def attend(self, layer, q, causal_unit=0, **more):
+    def attend(self, layer, q, causal_unit=0, stream=None, **more):
         """Attention of the step's rows over a layer's cache (see ``cached``)."""
-        return cached(q, *self.pages[layer], self.block_table, self.cu_rows, self.kv_lens, causal_unit, **more)
+        result = cached(q, *self.pages[layer], self.block_table, self.cu_rows, self.kv_lens, causal_unit,
+                        stream=stream, **more)
+        self._used_on(stream, *self.pages[layer], self.block_table, self.kv_lens)
+        return result
 
     def release(self, seq):
         """Gives the pages of sequence ``seq`` back and empties it (on torch's current stream)."""
@@ -692,7 +726,6 @@ class PagedCache:
         row, held = self.block_table[seq], (self.kv_lens[seq] + self.page_size - 1) // self.page_size
         col = torch.arange(row.numel(), device=row.device)
         at = torch.where(col < held, self.n_free + col, self.free_pages.numel() - 1)
-        self.free_pages = self.free_pages.index_put((at,), row)
-        self.n_free = (self.n_free + held).to(torch.int32)
-        self.kv_lens = self.kv_lens.clone()
+        self.free_pages.index_put_((at,), row)
+        self.n_free += held
         self.kv_lens[seq] = 0

@@ -215,11 +215,14 @@ void expect_args(Py_ssize_t n, Py_ssize_t want)
     TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n);
 }
 
-// entry, cached_lens, new_lens, free_pages, n_free, block_table, page_size, n_rows, n_pages, stream
+// entry, cached_lens, new_lens, free_pages, n_free, block_table, page_size, n_rows, n_pages, stream, step, state
+//
+// step (or None): where cu_rows and the slots go, [n_seqs + 1 + n_rows] at least.  state (or None): the counts and
+// kv_lens are copied there behind the kernel, [2 + n_seqs]; cached_lens and n_free may lie in it.
 PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    expect_args(n, 10);
+    expect_args(n, 12);
     const at::Tensor &cached = tensor(a[1], "cached_lens"), &fresh = tensor(a[2], "new_lens");
     const at::Tensor &free = tensor(a[3], "free_pages"), &n_free = tensor(a[4], "n_free");
     const at::Tensor &table = tensor(a[5], "block_table");
@@ -228,9 +231,13 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n)
                       "one cached length, new length and row of block_table per sequence, one n_free");
     TORCH_CHECK_VALUE(table.size(0) <= INT32_MAX && table.size(1) <= INT32_MAX && free.numel() <= INT32_MAX,
                       "a size outside the 32-bit range");
-    const Call call(table, "block_table", a[9]);
     const int64_t seqs = table.size(0);
     const int32_t rows = int32(a[7], "n_rows");
+    const int64_t step_size = seqs + 1 + std::max(rows, 0);
+    std::optional<at::Tensor> step = maybe(a[10], "step"), state = maybe(a[11], "state");
+    TORCH_CHECK_VALUE((!step || step->numel() >= step_size) && (!state || state->numel() == 2 + seqs),
+                      "step: [n_seqs + 1 + n_rows] at least, state: [2 + n_seqs]");
+    const Call call(table, "block_table", a[9]);
     vggt_cache c{};
     c.n_seqs = static_cast<int32_t>(seqs);
     c.n_heads = c.n_kv_heads = 1;
@@ -244,16 +251,27 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n)
     auto *in_free = static_cast<const int32_t *>(call.use(free, at::kInt, "free_pages"));
     auto *in_n_free = static_cast<const int32_t *>(call.use(n_free, at::kInt, "n_free"));
     auto *in_table = static_cast<int32_t *>(call.use(table, at::kInt, "block_table"));
-    // one buffer: every part starts on 4 bytes, which is all that is asked
-    const at::Tensor out = call.empty({2 * seqs + 3 + std::max(rows, 0)}, at::kInt);
-    int32_t *p = out.mutable_data_ptr<int32_t>();
+    // counts, lengths and the step in one buffer: every part starts on 4 bytes, which is all that is asked
+    const at::Tensor out = call.empty({2 + seqs + (step ? 0 : step_size)}, at::kInt);
+    int32_t *counts = out.mutable_data_ptr<int32_t>(), *lens = counts + 2;
+    int32_t *offsets = step ? static_cast<int32_t *>(call.use(step, at::kInt, "step")) : lens + seqs;
+    if (state)
+        call.use(state, at::kInt, "state");
     const vggt_status status = entry<decltype(vggt_cache_plan)>(a[0])(
-        c, in_cached, in_fresh, in_free, static_cast<int32_t>(free.numel()), in_n_free, in_table, rows, p + 2,
-        p + 3 + seqs, p + 3 + 2 * seqs, p, call.stream());
+        c, in_cached, in_fresh, in_free, static_cast<int32_t>(free.numel()), in_n_free, in_table, rows, offsets, lens,
+        offsets + seqs + 1, counts, call.stream());
     if (status != VGGT_OK)
         return results(status);
-    auto part = [&](int64_t at, int64_t size) { return wrap(out.as_strided({size}, {1}, at)); };
-    return results(status, part(2, seqs + 1), part(3 + seqs, seqs), part(3 + 2 * seqs, rows), part(0, 2));
+    if (state) {
+        // not by the kernel: it reads the old values while it writes the new ones
+        const c10::cuda::CUDAStreamGuard guard(call.other.value_or(call.current));
+        state->copy_(out.as_strided({2 + seqs}, {1}, 0));
+    }
+    const at::Tensor &in = step ? *step : out;
+    const int64_t first = step ? step->storage_offset() : 2 + seqs;
+    auto part = [](const at::Tensor &t, int64_t at, int64_t size) { return wrap(t.as_strided({size}, {1}, at)); };
+    return results(status, part(in, first, seqs + 1), part(out, 2, seqs), part(in, first + seqs + 1, rows),
+                   part(out, 0, 2));
     END_HANDLE_TH_ERRORS
 }
 

@@ -622,3 +622,107 @@ def test_streamed_block_matches_the_whole_scene():
     in_use = cache.block_table[0, :2].tolist() + cache.block_table[1, :-(-int(cache.kv_lens[1]) // page)].tolist()
     free = cache.free_pages[:int(cache.n_free)].tolist()
     assert sorted(in_use + free) == list(range(64))
+
+
+class Scenes:
+    """Sequences streamed through a PagedCache, and what their rows must give."""
+
+    def __init__(self, cache, heads, seed=1):
+        self.cache, self.heads, self.g = cache, heads, torch.Generator(device="cuda").manual_seed(seed)
+        self.kept = [[] for _ in range(cache.kv_lens.numel())]
+
+    def rows(self, n):
+        return torch.randn(n, self.heads, D, generator=self.g, device="cuda").bfloat16()
+
+    def check(self, new, q, k, v, got, unit=1):
+        """After a step of ``new`` rows per sequence."""
+        ends = [sum(new[:b]) for b in range(len(new) + 1)]
+        for b, kept in enumerate(self.kept):
+            kept.append((k[ends[b]:ends[b + 1]].clone(), v[ends[b]:ends[b + 1]].clone()))
+        ks, vs = ([torch.cat([x[i] for x in kept]) for kept in self.kept] for i in (0, 1))
+        kv = [len(x) for x in ks]
+        assert self.cache.kv_lens.tolist() == kv
+        want, _, spread = ref.attention(q[:ends[-1]], ks, vs, ends, kv, unit)
+        tol = 2.0 ** -8 * (1.01 * want.abs() + 1.12 * spread) + 1e-30
+        assert ((got[:ends[-1]].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("whole", [True, False])
+def test_a_captured_step_of_a_cache_goes_on_from_its_present_state(whole):
+    """A single-token step captured with its plan or without, replayed several times, with eager steps of other sizes
+    and a released sequence in between."""
+    heads, seqs = 4, 3
+    cache = attn.PagedCache(n_pages=60, page_size=8, n_kv_heads=heads, n_seqs=seqs, max_pages=30)
+    scenes = Scenes(cache, heads)
+
+    def eager(new, pad=0):
+        n = sum(new)
+        q, k, v = (scenes.rows(n + pad) for _ in range(3))
+        assert cache.plan(i32(new), n + pad).item() == 0
+        cache.append(0, k, v)
+        scenes.check(new, q, k, v, cache.attend(0, q, causal_unit=1))
+
+    eager([30, 5, 0])
+    ones, (q, k, v) = i32([1] * seqs), (scenes.rows(seqs) for _ in range(3))
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    if not whole:
+        cache.plan(i32([0] * seqs), seqs)  # the step's buffers are those of any plan of as many rows
+    with torch.cuda.graph(graph):
+        if whole:
+            refused = cache.plan(ones, seqs)
+        cache.append(0, k, v)
+        got = cache.attend(0, q, causal_unit=1)
+
+    def replay():
+        for t in (q, k, v):
+            t.copy_(scenes.rows(seqs))
+        if not whole:
+            assert cache.plan(ones, seqs).item() == 0
+        graph.replay()
+        ok()
+        assert not whole or refused.item() == 0
+        scenes.check([1] * seqs, q, k, v, got)
+
+    replay()
+    replay()
+    eager([0, 70, 9], pad=3)
+    for _ in range(9):
+        replay()
+    cache.release(0)
+    scenes.kept[0] = []
+    replay()
+    eager([11, 0, 0])
+    replay()
+    held = sum(-(-n // 8) for n in cache.kv_lens.tolist())
+    assert cache.n_free.item() == 60 - held
+
+
+def test_a_cache_planned_on_another_stream_behind_queued_work():
+    """What the plans read and write must outlast the host's calls: buffers of their sizes are taken and overwritten
+    on the current stream while the plans are still queued."""
+    heads, seqs = 2, 300
+    cache = attn.PagedCache(n_pages=2000, page_size=8, n_kv_heads=heads, n_seqs=seqs, max_pages=9)
+    side = torch.cuda.Stream()
+    new, rows = [1 + b % 3 for b in range(seqs)], 2 * seqs
+    fresh, work = i32(new), torch.randn(4096, 4096, device="cuda")
+    for sizes in range(4):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                work = (work @ work).clamp(-1, 1)
+        refused = [cache.plan(fresh, rows, stream=s) for s in (side, side.cuda_stream, side)]
+        scratch = [torch.full((n,), 12345, dtype=torch.int32, device="cuda")
+                   for n in (1, 2, seqs, seqs + 2, seqs + 1 + 1024, 2 * seqs + 3 + rows, rows) for _ in range(20)]
+        torch.cuda.current_stream().wait_stream(side)
+        del scratch
+        assert [r.item() for r in refused] == [0, 0, 0]
+        assert cache.kv_lens.tolist() == [3 * (sizes + 1) * n for n in new]
+        table, slots = cache.block_table.tolist(), []
+        for b, n in enumerate(new):
+            total = 3 * (sizes + 1) * n
+            slots += [table[b][t // 8] * 8 + t % 8 for t in range(total - n, total)]
+        assert cache.slots.tolist() == slots + [-1] * (rows - len(slots))
+    used = [p for b, n in enumerate(new) for p in table[b][:-(-12 * n // 8)]]
+    assert len(set(used)) == len(used) and cache.n_free.item() == 2000 - len(used)
+    assert sorted(used + cache.free_pages[:cache.n_free.item()].tolist()) == list(range(2000))

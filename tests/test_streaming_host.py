@@ -183,6 +183,42 @@ def test_binding_says_when_its_module_is_not_built(monkeypatch):
         attn.norm_residual(torch.zeros(2, 8))
 
 
+def fake_plan(what, function, cached, new, free, n_free, table, page, n_rows, n_pages, stream, step=None, state=None):
+    """The compiled module's plan by the plain reference, on the CPU."""
+    assert function == "plan"
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    filled, cu, kv, slots, counts = ref.plan(cached.tolist(), new.tolist(), free.tolist(), int(n_free),
+                                             table.tolist(), page, n_rows)
+    table.copy_(i32(filled))
+    step = torch.zeros(len(cu) + n_rows, dtype=torch.int32) if step is None else step
+    step[:len(cu) + n_rows] = i32(cu + slots)
+    if state is not None:
+        state.copy_(i32(counts + kv))
+    return 0, step[:len(cu)], i32(kv), step[len(cu):len(cu) + n_rows], i32(counts)
+
+
+def test_paged_cache_keeps_its_state_in_place(monkeypatch):
+    """What a queued plan reads is still the cache's own afterwards, and what a captured step reads is what later
+    steps update."""
+    monkeypatch.setattr(attn, "_call", fake_plan)
+    cache = attn.PagedCache(n_pages=7, page_size=8, n_kv_heads=1, n_seqs=2, max_pages=5, device="cpu")
+    state = lambda: [t.data_ptr() for t in (cache.kv_lens, cache.n_free, cache.free_pages, cache.block_table)]  # noqa: E731
+    new = lambda *n: torch.tensor(n, dtype=torch.int32)  # noqa: E731
+    first, steps, refused = state(), {}, []
+    for n, rows in (((9, 3), 12), ((1, 1), 2), ((0, 40), 40), ((1, 1), 2), ((7, 0), 12)):
+        refused.append(cache.plan(new(*n), rows))
+        assert state() == first
+        step = [cache.cu_rows.data_ptr(), cache.slots.data_ptr()]
+        assert steps.setdefault(rows, step) == step and cache.slots.numel() == rows
+    assert cache.kv_lens.tolist() == [18, 5] and cache.n_free.tolist() == [3]
+    assert [r.tolist() for r in refused] == [[0], [0], [1], [0], [0]]  # each step's own
+    cache.release(0)
+    assert state() == first
+    assert cache.kv_lens.tolist() == [0, 5] and cache.n_free.tolist() == [6]
+    held = cache.block_table[1, :1].tolist()
+    assert sorted(cache.free_pages[:6].tolist() + held) == list(range(7))
+
+
 def test_the_references_agree_with_hand_values():
     # two keys, logits 0 and ln 3: weights 1/4 and 3/4; the first row sees the first key alone
     q = torch.zeros(2, 1, 64)
