@@ -685,7 +685,8 @@ class PagedCache:
 
     def plan(self, new_lens, n_rows, stream=None):
         """Plans a step of new_lens rows (int32 [n_seqs], on the device) in buffers of n_rows rows; returns the
-        number of refused sequences (int32 [1], on the device)."""
+        number of refused sequences (int32 [1], on the device).  A refused sequence keeps its length, its rows are
+        not appended, and what attend() returns for them is to be discarded."""
         size = 1 << max(int(n_rows) - 1, 0).bit_length()
         step, device = self._steps.get(size), self._state.device
         if step is None:

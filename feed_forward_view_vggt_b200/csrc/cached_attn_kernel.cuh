@@ -380,8 +380,9 @@ __device__ __forceinline__ void drain_copies(CachedSmem &sm, const Issued &issue
 // reads 1.35 GB instead of 3.15 (0.56 are needed), 894 us instead of 938 alone and
 // 1039 instead of 1110 in a row, where the power cap sets the clock.  V is warp 3's:
 // the copies of a tile of small pages are many (16 of 2 KB for pages of 16),
-// and a warp issues those of its lanes one after another.  Units without keys (their sequence was
-// refused pages, e.g.) are dealt with here and never enter the ring.
+// and a warp issues those of its lanes one after another.  Units without keys (a first
+// chunk that was refused pages, e.g.) are dealt with here and never enter the
+// ring.
 __device__ __forceinline__ void walk_work(CachedSmem &sm, const CUtensorMap *tmQ, const CUtensorMap *tmK,
                                           const CachedParams &p, Issued &issued)
 {

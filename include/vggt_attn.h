@@ -388,7 +388,10 @@ typedef struct {
  * free_pages[n_free - 1] first.  A sequence is refused when its rows end
  * behind n_rows, when it would need more than max_pages pages, or when it
  * needs a page and its needs and those of the sequences before it exceed
- * n_free; it takes none.  The caller returns pages by writing them behind
+ * n_free; it takes none.  Its kv_lens entry stays at cached, its rows get no
+ * slot, and what vggt_attn_cached returns for them is to be discarded (they
+ * keep their place in cu_rows, so it takes them for the last cached positions;
+ * zeros and -inf if nothing is cached).  The caller returns pages by writing them behind
  * the last free one.  counts[0] may be the next step's *n_free; counts must
  * not overlap n_free (the same step can then be planned again).  The heads
  * and strides of `cache` are not used.  One kernel launch. */

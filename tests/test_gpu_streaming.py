@@ -624,6 +624,38 @@ def test_streamed_block_matches_the_whole_scene():
     assert sorted(in_use + free) == list(range(64))
 
 
+def test_a_refused_sequence_keeps_its_cache_and_leaves_the_others_alone():
+    """Three scenes with 20, 9 and 0 cached positions; then only the second one's rows fit the free pages.  The refused
+    one with a cache gets what its last cached positions see, the one without gets nothing."""
+    heads = 2
+    cache = attn.PagedCache(n_pages=5, page_size=8, n_kv_heads=heads, n_seqs=3, max_pages=9)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    r = lambda n: torch.randn(n, heads, D, generator=g, device="cuda").bfloat16()  # noqa: E731
+    k0, v0 = r(29), r(29)
+    assert cache.plan(i32([20, 9, 0]), 29).item() == 0 and cache.n_free.item() == 0
+    cache.append(0, k0, v0)
+    before = [p.clone() for p in cache.pages[0]]
+    new = [6, 3, 2]
+    q, k, v = r(11), r(11), r(11)
+    assert cache.plan(i32(new), 11).item() == 2
+    assert cache.kv_lens.tolist() == [20, 12, 0] and cache.cu_rows.tolist() == [0, 6, 9, 11]
+    assert (cache.slots[:6] == -1).all() and (cache.slots[9:] == -1).all()
+    cache.append(0, k, v)
+    got, lse = cache.attend(0, q, causal_unit=1, want_lse=True)
+    ok()
+    page = cache.block_table[1, 1].item()
+    for now, was, x in zip(cache.pages[0], before, (k, v)):
+        assert torch.equal(now[page, :, 1:4], x[6:9].transpose(0, 1))
+        now[page, :, 1:4] = was[page, :, 1:4]
+        assert torch.equal(now, was)
+    ks, vs = ([torch.cat([a[:20], b[:0]]), torch.cat([a[20:], b[6:9]]), a[:0]] for a, b in ((k0, k), (v0, v)))
+    want, want_lse, spread = ref.attention(q, ks, vs, [0, 6, 9, 11], [20, 12, 0], 1)
+    assert ((got.double() - want).abs() <= 2.0 ** -8 * (1.01 * want.abs() + 1.12 * spread) + 1e-30).all()
+    assert (got[9:] == 0).all() and torch.isneginf(lse[9:]).all()
+    cache.release(0)  # its pages are still its own
+    assert cache.n_free.item() == 3 and cache.plan(i32([0, 0, 2]), 2).item() == 0
+
+
 class Scenes:
     """Sequences streamed through a PagedCache, and what their rows must give."""
 
