@@ -54,11 +54,16 @@ def up_to_date(lib: str = LIB) -> bool:
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
     """Builds the release library, or with debug=True the library with
-    device index checks (-DVGGT_DEBUG); returns its path."""
+    device index checks (-DVGGT_DEBUG), then the torch-side module, which
+    alone needs torch and a host compiler; returns the library's path."""
     lib = DEBUG_LIB if debug else LIB
+    if force or not up_to_date(lib):
+        build_library(lib, verbose, debug)
     build_binding(force=force and not debug, verbose=verbose)
-    if not force and up_to_date(lib):
-        return lib
+    return lib
+
+
+def build_library(lib: str, verbose: bool = False, debug: bool = False) -> None:
     tmp = lib + ".tmp.%d" % os.getpid()
     cmd = [nvcc(), *NVCC_FLAGS, *(["-DVGGT_DEBUG"] if debug else []), "-I", INCLUDE, "-I", CSRC, "-o", tmp,
            *SOURCES]
@@ -67,7 +72,6 @@ def build(force: bool = False, verbose: bool = False, debug: bool = False) -> st
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, lib)
-    return lib
 
 
 def build_binding(force: bool = False, verbose: bool = False) -> str:

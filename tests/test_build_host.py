@@ -1,0 +1,41 @@
+"""What build() does in which order (CPU)."""
+import os
+
+import pytest
+
+from feed_forward_view_vggt_b200 import build as vbuild
+
+
+@pytest.fixture
+def commands(tmp_path, monkeypatch):
+    """The compiler calls of a build into an empty folder; each writes a file with its command line."""
+    ran = []
+
+    def run(cmd, check):
+        ran.append(cmd)
+        out = cmd[cmd.index("-o") + 1]
+        with open(out, "w") as f:
+            f.write("\n".join(cmd))
+
+    monkeypatch.setattr(vbuild.subprocess, "run", run)
+    for name in ("LIB", "DEBUG_LIB", "BINDING"):
+        monkeypatch.setattr(vbuild, name, str(tmp_path / os.path.basename(getattr(vbuild, name))))
+    return ran
+
+
+def test_the_library_is_built_where_the_module_cannot_be(commands, monkeypatch):
+    def no_torch(*a, **k):
+        raise ImportError("no torch here")
+
+    monkeypatch.setattr(vbuild, "build_binding", no_torch)
+    with pytest.raises(ImportError):
+        vbuild.build()
+    assert len(commands) == 1 and os.path.exists(vbuild.LIB)
+
+
+def test_a_build_does_what_is_missing(commands):
+    assert vbuild.build() == vbuild.LIB and len(commands) == 2
+    assert vbuild.build() == vbuild.LIB and len(commands) == 2
+    assert vbuild.build(debug=True) == vbuild.DEBUG_LIB and len(commands) == 3
+    vbuild.build(force=True)
+    assert len(commands) == 5
