@@ -577,7 +577,8 @@ def _call(what, function, *args):
         try:
             from . import _streaming
         except ImportError as e:
-            raise RuntimeError("_streaming.so is not built; run `python -m feed_forward_view_vggt_b200.build`") from e
+            raise RuntimeError(f"_streaming.so is not built, or not for this torch ({e}); run "
+                               "`python -m feed_forward_view_vggt_b200.build`") from e
         _host = _streaming
     result = getattr(_host, function)(_entry(what), *args)
     status = result if isinstance(result, int) else result[0]

@@ -74,10 +74,27 @@ def build_library(lib: str, verbose: bool = False, debug: bool = False) -> None:
     os.replace(tmp, lib)
 
 
+def binding_is_for() -> str:
+    """What the torch-side module is built for; it holds these words."""
+    import torch
+
+    return "built for torch %s, abi %d, %s" % (torch.__version__, torch._C._GLIBCXX_USE_CXX11_ABI,
+                                               sys.implementation.cache_tag)
+
+
+def binding_up_to_date() -> bool:
+    if not os.path.exists(BINDING):
+        return False
+    deps = [BINDING_SOURCE] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
+    if any(os.path.getmtime(BINDING) < os.path.getmtime(p) for p in deps):
+        return False
+    with open(BINDING, "rb") as f:
+        return binding_is_for().encode() in f.read()
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """Builds the torch-side module of the streaming calls; returns its path."""
-    deps = [BINDING_SOURCE] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(BINDING) >= os.path.getmtime(p) for p in deps):
+    if not force and binding_up_to_date():
         return BINDING
     import sysconfig
 
@@ -88,6 +105,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
     tmp = BINDING + ".tmp.%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           '-DVGGT_BUILT_FOR="%s"' % binding_is_for(),
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], "-I", INCLUDE,

@@ -413,11 +413,21 @@ PyMethodDef methods[] = {
     {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(norm)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
+#ifndef VGGT_BUILT_FOR
+#define VGGT_BUILT_FOR "built by hand"
+#endif
+
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_streaming", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 } // namespace
 
 PyMODINIT_FUNC PyInit__streaming()
 {
-    return PyModule_Create(&module);
+    PyObject *m = PyModule_Create(&module);
+    // torch's and Python's versions; the build looks for them to see whether the module is theirs
+    if (m && PyModule_AddStringConstant(m, "built_for", VGGT_BUILT_FOR) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
 }

@@ -1,4 +1,4 @@
-"""What build() does in which order (CPU)."""
+"""What build() does in which order, and when the torch-side module counts as current (CPU)."""
 import os
 
 import pytest
@@ -39,3 +39,22 @@ def test_a_build_does_what_is_missing(commands):
     assert vbuild.build(debug=True) == vbuild.DEBUG_LIB and len(commands) == 3
     vbuild.build(force=True)
     assert len(commands) == 5
+
+
+def test_the_module_is_rebuilt_for_another_torch(commands, monkeypatch):
+    import torch
+
+    vbuild.build()
+    monkeypatch.setattr(torch, "__version__", "99.0")
+    vbuild.build()
+    assert len(commands) == 3 and "99.0" in " ".join(commands[2])
+    vbuild.build()
+    assert len(commands) == 3
+
+
+def test_the_built_module_says_what_it_is_for():
+    vbuild.build()
+    import torch  # noqa: F401
+    from feed_forward_view_vggt_b200 import _streaming
+
+    assert _streaming.built_for == vbuild.binding_is_for()
