@@ -627,7 +627,7 @@ def cache_plan(cached_lens, new_lens, free_pages, n_free, block_table, page_size
 
 def cache_append(k, v, slots, k_pages, v_pages, stream=None):
     """Writes the rows of k and v ([n_rows, n_kv_heads, 64], rows and heads may
-    be strided) into their slots of k_pages and v_pages."""
+    be strided, alike in both) into their slots of k_pages and v_pages."""
     _call("vggt_cache_append", "append", k, v, slots, k_pages, v_pages, stream)
 
 

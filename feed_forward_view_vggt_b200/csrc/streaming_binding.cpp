@@ -147,10 +147,20 @@ struct Call {
     }
 };
 
+// Of the same sizes, with elements at the same places: a dimension of one element has no stride of its own.
+bool alike(const at::Tensor &a, const at::Tensor &b)
+{
+    if (a.sizes() != b.sizes())
+        return false;
+    for (int64_t d = 0; d < a.dim(); ++d)
+        if (a.size(d) > 1 && a.stride(d) != b.stride(d))
+            return false;
+    return true;
+}
+
 vggt_cache page_layout(const at::Tensor &k, const at::Tensor &v, int64_t n_heads, int64_t n_seqs, int64_t max_pages)
 {
-    TORCH_CHECK_VALUE(k.dim() == 4 && k.sizes() == v.sizes() && k.strides() == v.strides() &&
-                          (k.stride(3) == 1 || k.size(3) == 1),
+    TORCH_CHECK_VALUE(k.dim() == 4 && alike(k, v) && (k.stride(3) == 1 || k.size(3) == 1),
                       "k_pages, v_pages: [n_pages, n_kv_heads, page_size, head_dim] of the same strides, the last one 1");
     for (int64_t n : {k.size(0), k.size(1), k.size(2), k.size(3), n_heads, n_seqs, max_pages})
         TORCH_CHECK_VALUE(n <= INT32_MAX, "a size outside the 32-bit range");
@@ -282,8 +292,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n)
     expect_args(n, 7);
     const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &slots = tensor(a[3], "slots");
     const at::Tensor &k_pages = tensor(a[4], "k_pages"), &v_pages = tensor(a[5], "v_pages");
-    TORCH_CHECK_VALUE(k.dim() == 3 && k.sizes() == v.sizes() && k.strides() == v.strides() && slots.dim() == 1 &&
-                          slots.size(0) == k.size(0),
+    TORCH_CHECK_VALUE(k.dim() == 3 && alike(k, v) && slots.dim() == 1 && slots.size(0) == k.size(0),
                       "k, v: [n_rows, n_kv_heads, head_dim] of the same strides, one slot per row");
     const vggt_cache c = page_layout(k_pages, v_pages, k.size(1), 1, 1);
     TORCH_CHECK_VALUE(k.size(1) == c.n_kv_heads && k.size(2) == c.head_dim && k.size(0) <= INT32_MAX,

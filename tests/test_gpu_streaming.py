@@ -120,6 +120,23 @@ def test_append(layout, rows, heads, page):
         assert torch.equal(got.contiguous().view(torch.int16), exp.contiguous().view(torch.int16))
 
 
+def test_append_of_one_row_and_one_page_of_other_strides():
+    heads, page = 3, 8
+    g = torch.Generator(device="cuda").manual_seed(8)
+    r = lambda *n: torch.randn(*n, generator=g, device="cuda").bfloat16()  # noqa: E731
+    k, v = r(1, heads, D), r(1, 3, heads, D)[:, 1]
+    k_pages, v_all = r(1, heads, page, D), r(7, 2, heads, page, D)
+    v_pages = v_all[3:4, 1]
+    want_k, want_v = k_pages.clone(), v_all.clone()
+    want_k[0, :, 5], want_v[3, 1, :, 5] = k[0], v[0]
+    attn.cache_append(k, v, i32([5]), k_pages, v_pages)
+    got = attn.cached(k, k_pages, v_pages, i32([[0]]), i32([0, 1]), i32([6]))
+    ok()
+    assert torch.equal(k_pages, want_k) and torch.equal(v_all, want_v)
+    want, _, spread = ref.attention(k, [want_k[0].transpose(0, 1)], [want_v[3, 1].transpose(0, 1)], [0, 1], [6], 0)
+    assert ((got.double() - want).abs() <= 2.0 ** -8 * (1.01 * want.abs() + 1.12 * spread) + 1e-30).all()
+
+
 def test_append_reports_and_skips_a_slot_outside_the_cache():
     k_pages, v_pages = (torch.zeros(2, 2, 8, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     k = torch.ones(3, 2, D, dtype=torch.bfloat16, device="cuda")

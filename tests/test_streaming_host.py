@@ -173,6 +173,30 @@ def test_binding_checks_its_tensors():
         attn.norm_residual(torch.zeros(2, 8), gate=torch.zeros(2, 8), rows_per_gate=2)
 
 
+@pytest.mark.parametrize("rows,heads", [(1, 3), (4, 1), (1, 1)])
+def test_binding_takes_any_stride_of_a_dimension_of_one(rows, heads):
+    # a row of a projection beside a row of its own, one page or head of a larger cache: accepted up to the device
+    k, v = torch.zeros(rows, heads, 64).bfloat16(), torch.zeros(rows, 3, heads, 64).bfloat16()[:, 1]
+    if rows > 1:
+        k = torch.zeros(rows, 3, 5, 64).bfloat16()[:, 1, :1]
+        v = torch.zeros(rows, 3, 1, 320).bfloat16()[:, 1, :, :64]
+    pages = torch.zeros(1, heads, 8, 64).bfloat16()
+    others = torch.zeros(7, 2, heads, 8, 64).bfloat16()[3:4, 1]
+    assert k.stride() != v.stride() and pages.stride() != others.stride()
+    with pytest.raises(ValueError, match="k_pages: tensor must live on a CUDA device"):
+        attn.cache_append(k, v, torch.zeros(rows, dtype=torch.int32), pages, others)
+
+
+def test_binding_refuses_rows_that_lie_differently():
+    k, v = torch.zeros(4, 3, 64).bfloat16(), torch.zeros(4, 3, 3, 64).bfloat16()[:, 1]
+    pages = torch.zeros(2, 3, 8, 64).bfloat16()
+    with pytest.raises(ValueError, match="same strides"):
+        attn.cache_append(k, v, torch.zeros(4, dtype=torch.int32), pages, pages.clone())
+    with pytest.raises(ValueError, match="same strides"):
+        attn.cache_append(k, k, torch.zeros(4, dtype=torch.int32), pages,
+                          torch.zeros(2, 8, 3, 64).bfloat16().transpose(1, 2))
+
+
 def test_binding_says_when_its_module_is_not_built(monkeypatch):
     import sys
 
