@@ -131,7 +131,10 @@ def load_library(path: str):
         "vggt_norm_residual": ([vggt_norm, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], i32),
     }
     for name, (args, res) in sigs.items():
-        fn = getattr(lib, name)
+        # entry points were added without a new version: an older library may report the same one
+        fn = getattr(lib, name, None)
+        if fn is None:
+            raise RuntimeError(f"{path} has no {name}; rebuild it")
         fn.argtypes = args
         fn.restype = res
     if lib.vggt_abi_version() != ABI_VERSION:

@@ -1,8 +1,11 @@
-"""What build() does in which order, and when the torch-side module counts as current (CPU)."""
+"""What build() does in which order, when the torch-side module counts as current and what loading an older library
+says (CPU)."""
 import os
+import subprocess
 
 import pytest
 
+from feed_forward_view_vggt_b200 import attn
 from feed_forward_view_vggt_b200 import build as vbuild
 
 
@@ -58,3 +61,13 @@ def test_the_built_module_says_what_it_is_for():
     from feed_forward_view_vggt_b200 import _streaming
 
     assert _streaming.built_for == vbuild.binding_is_for()
+
+
+def test_a_library_of_the_same_version_without_an_entry_point_is_refused(tmp_path):
+    lib = str(tmp_path / "old.so")
+    older = [n for n in attn.declared_symbols() if n != "vggt_attn_cached"]
+    code = "".join(f"int {n}(void) {{ return {attn.ABI_VERSION}; }}\n" for n in older)
+    subprocess.run([os.environ.get("CC", "gcc"), "-shared", "-fPIC", "-x", "c", "-", "-o", lib], input=code.encode(),
+                   check=True)
+    with pytest.raises(RuntimeError, match="no vggt_attn_cached; rebuild"):
+        attn.load_library(lib)
