@@ -70,7 +70,8 @@ constexpr int kCachedPolyPairs = 2;
 constexpr int kTaskRing = 8;
 
 constexpr int kFewRows = 16;      // rows of a task that the warps work on by themselves
-constexpr int kSoftmaxWarps = 8;  // and with how many: 16 keys of a tile each
+constexpr int kSoftmaxWarps = 8;  // and with how many: 32 keys of every other tile each
+static_assert(kStages % 2 == 0, "a warp of such a task waits for every other tile and must see every phase of its slots");
 
 enum : uint32_t { kSiteTaskFull = 12, kSiteTaskEmpty, kSiteMergeReady, kSiteMergeFree, kSiteFewQ, kSiteFewFull, kSiteTaskPassed };
 
@@ -530,6 +531,7 @@ __device__ __forceinline__ void run_v_producer(CachedSmem &sm, const CUtensorMap
 // when the warps are done (fews_over).  Twice the slots of the task ring keep
 // the phases of `task_passed` apart: an issuer has left task it - 16 when task
 // it appears in the ring, and cannot reach it + 16 before the warps release it + 8.
+// (tests/cached_protocol_model.py runs the barriers under random timings.)
 __device__ __forceinline__ void pass_task(CachedSmem &sm, int it)
 {
     mbar_arrive(smem_u32(&sm.task_passed[it % (2 * kTaskRing)]));
