@@ -102,6 +102,11 @@ def test_traffic_record_requires_matching_kernel_source(tmp_path, monkeypatch):
     assert bench.recorded_traffic() == 123.0
 
 
+def test_traffic_record_is_of_the_present_kernel():
+    # else the bench reports no DRAM traffic: capture it again, the record says how
+    assert bench.recorded_traffic() is not None
+
+
 def test_workload_flops_n100():
     from feed_forward_view_vggt_b200 import synth
 
