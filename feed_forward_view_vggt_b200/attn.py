@@ -8,6 +8,9 @@ passed) or raw integer device addresses; ``stream`` may be a
 current stream.  The library is loaded on first use; if it has not been
 built this raises -- there is no CPU fallback.
 
+Tensors given to a call on another stream than torch's current one must live
+until that stream is past the call (or be recorded on it).
+
 The helpers at the bottom (``frame``, ``global_``, ``sga``, ``cached``, ...) allocate the
 outputs with torch, call the entry points and raise ``VggtError`` on a
 non-zero status.

@@ -36,11 +36,17 @@
 // Bound by the exponentials and the instructions around them, as that kernel
 // is: one frame of 1374 tokens over 100 cached ones, 16 heads, 0.89 ms or 870
 // TFLOP/s alone, 1.04 ms or 750 in a row under the power cap.  Single tokens are
-// bound by HBM: 148 sequences of 32000 keys 6.9 TB/s, 48 of odd lengths in pages
-// of 16, with grouped heads, 178 us or 4.8 TB/s.  Small calls are bound by
+// bound by HBM: 148 sequences of 32000 keys 6.9 TB/s, 48 of odd lengths with
+// grouped heads 134 us or 6.4 TB/s in pages of 128; small pages by their many
+// copies, 137 us in pages of 64, 151 of 32, 175 of 16.  Small calls are bound by
 // latency: planning 0.8 us, finding the first task 1.2 us, first keys 1.5 us,
 // the end of a task 1.5 us, the joining launch 2 us (one token over 5496 keys
 // and 16 heads: 12 us in a graph).
+//
+// P is rounded to bf16 for the PV product, whose operands have one type (each p
+// off by at most 2^-8 of itself; over all outputs 0.0016 of their size, beside
+// 0.0017 from the rounding of O); the sums l and O are fp32, l of P before it is
+// rounded.
 //
 // Keys behind kv are never used, whatever the page holds there: their scores
 // are masked, their V rows are zeroed in shared memory up to the next multiple

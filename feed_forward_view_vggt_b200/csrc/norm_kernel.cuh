@@ -148,8 +148,9 @@ __device__ __forceinline__ void normalise(const NormParams &p, float (&t)[8], bo
 
 // One warp per 256 channels of a row, 8 channels per thread, the row in
 // registers; kWarps = 1: four rows per block, else the block is a row's.  Many
-// rows are bound by HBM (x, y, x' and h once each; 137400 x 1024, fp32 x: 264
-// us, 6.4 TB/s; with 32 channels per thread and a warp per row 266-268).  Few
+// rows are bound by HBM (x, y, x' and h once each; 137400 x 1024, fp32 x: 272
+// us alone, 6.2 TB/s, and 282 to 301 in a row; 32 channels per thread and a warp
+// per row were 1% slower).  Few
 // rows (kAhead) are bound by the latency of a trip to memory and of the sums:
 // every load is issued at the start (17 x 1024: 6 us instead of 12).
 template <typename X, int kWarps, bool kAhead>

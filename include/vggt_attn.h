@@ -423,7 +423,8 @@ vggt_status vggt_cache_append(vggt_cache cache, const void *k, const void *v, in
  * A row that sees no key gets o = 0 and lse = -inf.  Rows behind
  * cu_rows[n_seqs] are not written.  Cache contents behind kv_lens[b] are
  * never used, whatever they hold; keys and values before it must be finite
- * (a non-finite value can reach rows that do not see its key).
+ * (a non-finite value can reach rows that do not see its key, and a NaN among
+ * the keys need not show in rows that do).
  * q: bf16, row r, head h at r * q_row_stride + h * q_head_stride (elements,
  * multiples of 8, at least 64).  o: bf16 [n_rows, H, 64].  lse: optional
  * float [n_rows, H].  block_table: int32 [n_seqs, max_pages], its first
