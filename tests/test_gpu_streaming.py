@@ -137,6 +137,24 @@ def test_append_of_one_row_and_one_page_of_other_strides():
     assert ((got.double() - want).abs() <= 2.0 ** -8 * (1.01 * want.abs() + 1.12 * spread) + 1e-30).all()
 
 
+@pytest.mark.parametrize("unit", [0, 1, 2 ** 31 - 1])
+def test_head_major_rows(unit):
+    # q, k and v as [heads, rows, 64]: rows lie 64 elements apart, heads further
+    b = ref.Batch([300, 41], [37, 2], 16, 6, 3, seed=12)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn(3, 39, D, generator=g, device="cuda").bfloat16().transpose(0, 1) for _ in range(2))
+    slots = torch.tensor([b.table[i, t // 16].item() * 16 + t % 16 for i, (n, m) in enumerate(zip(b.kv, b.new))
+                          for t in range(n - m, n)], dtype=torch.int32, device="cuda")
+    attn.cache_append(k, v, slots, b.k_pages, b.v_pages)
+    for i in range(2):
+        for seqs, x in ((b.k_seqs, k), (b.v_seqs, v)):
+            seqs[i][b.kv[i] - b.new[i]:] = x[b.cu[i]:b.cu[i + 1]]
+    q = b.q.transpose(0, 1).contiguous().transpose(0, 1)
+    got, lse = attn.cached(q, b.k_pages, b.v_pages, b.table, b.cu_rows, b.kv_lens, causal_unit=unit, want_lse=True)
+    ok()
+    check_attention(b, unit, got, lse)
+
+
 def test_append_reports_and_skips_a_slot_outside_the_cache():
     k_pages, v_pages = (torch.zeros(2, 2, 8, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
     k = torch.ones(3, 2, D, dtype=torch.bfloat16, device="cuda")
@@ -573,6 +591,22 @@ def test_norm_residual_without_h_and_of_a_constant_row():
     got, h = attn.norm_residual(x, y, kind="rms", eps=0.0)
     assert (h == 1).all()
     ok()
+
+
+@pytest.mark.parametrize("xt,rows,cols", [(torch.float32, 300, 520), (torch.bfloat16, 9, 2048)])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_norm_residual_of_a_strided_stream(xt, rows, cols, inplace):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    wide = torch.randn(rows, 2, cols, generator=g, device="cuda").to(xt)
+    x, beside = wide[:, 1], wide[:, 0].clone()
+    y = torch.randn(rows, cols, generator=g, device="cuda").bfloat16()
+    want_x = x.double() + y.double()
+    want_h = ref.normed(want_x, "rms", 1e-6, None, None)
+    got, h = attn.norm_residual(x, y, kind="rms", inplace=inplace)
+    ok()
+    assert (got is x) == inplace and torch.equal(wide[:, 0], beside)
+    assert ((got.double() - want_x).abs() <= norm_tolerance(2, "rms", 1e-6, want_x, xt)).all()
+    assert ((h.double() - want_h).abs() <= norm_tolerance(4, "rms", 1e-6, want_h, torch.bfloat16)).all()
 
 
 def test_norm_residual_keeps_a_large_offset():
